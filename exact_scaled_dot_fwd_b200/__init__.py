@@ -15,6 +15,7 @@ import os
 
 __all__ = ["attn_fwd", "attn_fwd_ws", "attn_workspace_size", "attn_set_workspace",
            "attn_fwd_paged", "attn_fwd_rope", "attn_fwd_decode_static", "rope_apply",
+           "paged_plan", "kv_append", "attn_fwd_tree", "attn_tree_workspace_size",
            "prefill_tile_shape", "tile_plan", "prefill_trace", "device_status", "attn_last_device_status",
            "AttnError", "lib", "STATUS_NAMES"]
 
@@ -88,6 +89,17 @@ def lib():
         L.attn_fwd_decode_static.restype = i
         L.attn_decode_static_max_bytes.argtypes = []
         L.attn_decode_static_max_bytes.restype = sz
+        ll = ctypes.POINTER(ctypes.c_int64)
+        L.paged_plan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
+        L.paged_plan.restype = i
+        L.kv_append.argtypes = [vp, vp, vp, ll, vp, f, i, vp, vp, vp, vp, vp, i, i, i, i, i, i, i,
+                                vp]
+        L.kv_append.restype = i
+        L.attn_fwd_tree.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
+                                    i, f, vp, vp, sz, vp]
+        L.attn_fwd_tree.restype = i
+        L.attn_tree_workspace_size.argtypes = [i, i, i, i, i]
+        L.attn_tree_workspace_size.restype = sz
         L.attn_debug_timeout_probe.argtypes = [ctypes.c_ulonglong, vp]
         L.attn_debug_timeout_probe.restype = i
         _lib = L
@@ -402,6 +414,218 @@ def rope_apply(x, base=10000.0, pos_offset=0, pairing=0, out=None, stream=None):
                               int(pairing), _stream(stream))
     _raise(rc, "rope_apply")
     return out
+
+
+def _used_on(stream, *tensors):
+    """Mark tensors allocated here (on the current stream) as used by
+    `stream`, so that the caching allocator keeps their memory until `stream`
+    has passed the call."""
+    torch = _torch()
+    s = _torch_stream(stream)
+    for t in tensors:
+        if t is not None and s != torch.cuda.current_stream(t.device):
+            t.record_stream(s)
+
+
+def _check_shape(t, name, dtype, shape):
+    _check_tensor(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N, index=None,
+               slots=None, state_out=None, stream=None):
+    """Pages and cache slots of one step: sequence b goes from old_lens[b] to
+    new_lens[b] tokens (int32 [B]).  block_table int32 [B, max_pages] and the
+    queue of free pages (free_pages int32 [num_pages], state int32 [2] =
+    {head, count}) are updated: growing sequences take pages from the queue's
+    head, shrinking ones give theirs back at its tail.  Returns (slots,
+    state_out): slots int32 [B, N], the cache slot of the sequence's new token
+    i (or index[b, i], int32 [B, N], where given; negative: none), -1 where
+    there is none; state_out int32 [2], the queue's new state (a tensor of its
+    own: pass it as the next call's state).  Page shortage is reported by
+    device_status() (ATTN_ERANGE)."""
+    torch = _torch()
+    _check_tensor(block_table, "block_table", torch.int32, 2)
+    B, max_pages = block_table.shape
+    _check_shape(old_lens, "old_lens", torch.int32, (B,))
+    _check_shape(new_lens, "new_lens", torch.int32, (B,))
+    _check_tensor(free_pages, "free_pages", torch.int32, 1)
+    _check_shape(state, "state", torch.int32, (2,))
+    if index is not None:
+        _check_shape(index, "index", torch.int32, (B, N))
+    if slots is not None:
+        _check_shape(slots, "slots", torch.int32, (B, N))
+    if state_out is not None:
+        _check_shape(state_out, "state_out", torch.int32, (2,))
+    _check_devices(block_table, [(old_lens, "old_lens"), (new_lens, "new_lens"),
+                                 (free_pages, "free_pages"), (state, "state"), (index, "index"),
+                                 (slots, "slots"), (state_out, "state_out")])
+    with torch.cuda.device(block_table.device):
+        if slots is None:
+            slots = torch.empty((B, N), dtype=torch.int32, device=block_table.device)
+            _used_on(stream, slots)
+        if state_out is None:
+            state_out = torch.empty_like(state)
+            _used_on(stream, state_out)
+        rc = lib().paged_plan(_ptr(old_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_pages),
+                              _ptr(state), _ptr(state_out), _ptr(index), _ptr(slots), B, N,
+                              max_pages, int(page_size), free_pages.numel(), _stream(stream))
+    _raise(rc, "paged_plan")
+    return slots, state_out
+
+
+def _check_rows(t, name, shape):
+    """A bf16 [B, H, N, d] argument that may be a strided view with d
+    contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def kv_append(k, v=None, slots=None, k_cache=None, v_cache=None, q=None, positions=None,
+              rope_base=10000.0, rope_pairing=0, return_k=None, q_out=None, k_out=None,
+              stream=None):
+    """Rotate a step's queries and keys at each token's own position and store
+    its keys and values in the cache, in one pass.
+
+    q bf16 [B, Hq, N, d] or None, k and v bf16 [B, Hkv, N, d], strided views
+    allowed (d contiguous, other strides multiples of 8 elements); positions
+    int32 [B, N] or None (nothing is rotated); slots int32 [B, N] (paged_plan's;
+    negative: not stored) with k_cache, v_cache bf16 [num_pages, Hkv,
+    page_size, d] (a contiguous cache [B, Hkv, Nk, d] is B pages of Nk rows), or
+    None together with v and the caches: nothing is stored.  Slots must be
+    distinct.  Returns (q rotated or None, k rotated or None), contiguous; k's
+    is made when return_k is set (by default: when nothing is stored) or k_out
+    is given.  q_out / k_out may be q / k themselves."""
+    torch = _torch()
+    _check_rows(k, "k", None)
+    B, Hkv, N, d = k.shape
+    Hq = 0
+    if q is not None:
+        _check_rows(q, "q", None)
+        if (q.shape[0], q.shape[2], q.shape[3]) != (B, N, d):
+            raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)}")
+        Hq = q.shape[1]
+        if positions is None:
+            raise ValueError("kv_append rotates q: it needs positions")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if len({x is None for x in (v, slots, k_cache, v_cache)}) != 1:
+        raise ValueError("v, slots, k_cache and v_cache go together")
+    num_pages = page_size = 0
+    if slots is not None:
+        _check_rows(v, "v", k.shape)
+        _check_shape(slots, "slots", torch.int32, (B, N))
+        _check_tensor(k_cache, "k_cache", torch.bfloat16, 4)
+        _check_shape(v_cache, "v_cache", torch.bfloat16, k_cache.shape)
+        num_pages, hc, page_size, dc = k_cache.shape
+        if (hc, dc) != (Hkv, d):
+            raise ValueError(f"cache {tuple(k_cache.shape)} does not match k{tuple(k.shape)}")
+    if positions is not None:
+        _check_shape(positions, "positions", torch.int32, (B, N))
+    if return_k is None:
+        return_k = slots is None
+    if k_out is not None or return_k:
+        if positions is None:
+            raise ValueError("kv_append returns rotated keys: it needs positions")
+    if q_out is not None:
+        _check_shape(q_out, "q_out", torch.bfloat16, q.shape)
+    if k_out is not None:
+        _check_shape(k_out, "k_out", torch.bfloat16, k.shape)
+    _check_devices(k, [(q, "q"), (v, "v"), (slots, "slots"), (k_cache, "k_cache"),
+                       (v_cache, "v_cache"), (positions, "positions"), (q_out, "q_out"),
+                       (k_out, "k_out")])
+    strides = (ctypes.c_int64 * 9)(*[t.stride(j) if t is not None else 0
+                                     for t in (q, k, v) for j in range(3)])
+    with torch.cuda.device(k.device):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _used_on(stream, q_out)
+        if return_k and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            _used_on(stream, k_out)
+        rc = lib().kv_append(_ptr(q), _ptr(k), _ptr(v), strides, _ptr(positions),
+                             float(rope_base), int(rope_pairing), _ptr(q_out), _ptr(k_out),
+                             _ptr(slots), _ptr(k_cache), _ptr(v_cache), B, Hq, Hkv, N, d,
+                             page_size, num_pages, _stream(stream))
+    _raise(rc, "kv_append")
+    return q_out, k_out
+
+
+def attn_tree_workspace_size(B, Hq, Hkv, Nq, d) -> int:
+    return int(lib().attn_tree_workspace_size(B, Hq, Hkv, Nq, d))
+
+
+def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens=None,
+                  block_table=None, scale=None, workspace=None, out=None, lse=None,
+                  return_lse=True, stream=None):
+    """Attention for a tree of drafted tokens over a cache: q bf16 [B, Hq, Nq,
+    d], the nodes' keys (rotated) and values k_new, v_new bf16 [B, Hkv, Nq,
+    d], parents int32 [B, Nq] (the node each one follows, -1: the last cached
+    token; parents come first), new_lens int32 [B] nodes per sequence (None:
+    Nq).  Every node sees the key_lens[b] cached keys, itself and its
+    ancestors.  The cache is paged with a block_table int32 [B, max_pages]
+    (k_cache, v_cache bf16 [num_pages, Hkv, page_size, d]), else contiguous
+    [B, Hkv, Nk, d] (key_lens None: Nk).  Returns (o, lse) as attn_fwd; rows at
+    or beyond new_lens[b] are 0 and -inf."""
+    torch = _torch()
+    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (k_new, "k_new"),
+                 (v_new, "v_new")):
+        _check_tensor(t, n, torch.bfloat16, 4)
+    B, Hq, Nq, d = q.shape
+    Hkv = k_new.shape[1]
+    if tuple(k_new.shape) != (B, Hkv, Nq, d) or tuple(v_new.shape) != (B, Hkv, Nq, d):
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} k_new{tuple(k_new.shape)} "
+                         f"v_new{tuple(v_new.shape)}")
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or k_cache.shape[1] != Hkv \
+            or k_cache.shape[3] != d:
+        raise ValueError(f"cache shapes {tuple(k_cache.shape)}, {tuple(v_cache.shape)} do not "
+                         f"match k_new{tuple(k_new.shape)}")
+    max_pages = num_pages = page_size = Nk = 0
+    if block_table is not None:
+        _check_tensor(block_table, "block_table", torch.int32, 2)
+        if block_table.shape[0] != B:
+            raise ValueError(f"block_table has {block_table.shape[0]} rows, expected B = {B}")
+        if key_lens is None:
+            raise ValueError("attn_fwd_tree over a paged cache needs key_lens")
+        max_pages, num_pages, page_size = block_table.shape[1], k_cache.shape[0], k_cache.shape[2]
+    else:
+        if k_cache.shape[0] != B:
+            raise ValueError(f"cache has {k_cache.shape[0]} sequences, expected B = {B}")
+        Nk = k_cache.shape[2]
+    _check_shape(parents, "parents", torch.int32, (B, Nq))
+    if new_lens is not None:
+        _check_shape(new_lens, "new_lens", torch.int32, (B,))
+    _check_workspace(workspace)
+    _check_io(q, key_lens, out, lse if return_lse else None, B, Hq, Nq,
+              extra=[(k_cache, "k_cache"), (v_cache, "v_cache"), (k_new, "k_new"),
+                     (v_new, "v_new"), (parents, "parents"), (new_lens, "new_lens"),
+                     (block_table, "block_table"), (workspace, "workspace")])
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with torch.cuda.device(q.device):
+        made = [out is None, return_lse and lse is None]
+        out, lse = _outputs(q, out, lse, return_lse, B, Hq, Nq)
+        _used_on(stream, *(t for t, m in zip((out, lse), made) if m))
+        if workspace is None:
+            workspace = _scratch(attn_tree_workspace_size(B, Hq, Hkv, Nq, d), q.device, stream)
+        rc = lib().attn_fwd_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                 max_pages, page_size, num_pages, _ptr(k_new), _ptr(v_new),
+                                 _ptr(parents), _ptr(new_lens), _ptr(out),
+                                 _ptr(lse if return_lse else None), B, Hq, Hkv, Nq, Nk, d,
+                                 float(scale), _ptr(key_lens), _ptr(workspace),
+                                 workspace.numel(), _stream(stream))
+    _raise(rc, "attn_fwd_tree")
+    return (out, lse) if return_lse else out
 
 
 def prefill_tile_shape(d):

@@ -87,6 +87,20 @@ int check_common(const void* q, const void* k, const void* v, const void* o, int
   return ATTN_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Whether rows [B, H, N, d] with these strides (elements, >= 0) are contiguous.
+bool rows_contiguous(const int64_t* s, int B, int H, int N, int d) {
+  return (N == 1 || s[2] == d) && (H == 1 || s[1] == (int64_t)N * d) &&
+         (B == 1 || s[0] == (int64_t)H * N * d);
+}
+
+// Whether bytes [p, p + pn) and [q, q + qn) share any.
+bool ranges_meet(const void* p, size_t pn, const void* q, size_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + qn && b < a + pn;
+}
+
 }  // namespace
 
 int make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
@@ -161,7 +175,7 @@ const char* attn_strerror(int status) {
     case ATTN_EWORKSPACE: return "ATTN_EWORKSPACE: workspace missing or too small";
     case ATTN_ECUDA: return "ATTN_ECUDA: CUDA call failed";
     case ATTN_ETIMEOUT: return "ATTN_ETIMEOUT: a kernel gave up waiting on a barrier";
-    case ATTN_ERANGE: return "ATTN_ERANGE: a kernel met an out-of-range block-table entry";
+    case ATTN_ERANGE: return "ATTN_ERANGE: a kernel met an out-of-range table entry, slot or parent";
     default: return "unknown attn status";
   }
 }
@@ -372,6 +386,144 @@ int rope_apply(const void* x_in, void* x_out, int B, int H, int N, int d, float 
   if (a0 != b0 && a0 < b0 + bytes && b0 < a0 + bytes) return ATTN_EINVAL;   // partial overlap
   return launch_rope(x_in, x_out, B, H, N, d, base, pos_offset, pairing,
                      static_cast<cudaStream_t>(stream));
+}
+
+int paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t* block_table,
+               int32_t* free_pages, const int32_t* state_in, int32_t* state_out,
+               const int32_t* index, int32_t* slots, int B, int N, int max_pages, int page_size,
+               int num_pages, void* stream) {
+  if (!old_lens || !new_lens || !block_table || !free_pages || !state_in || !state_out || !slots)
+    return ATTN_EINVAL;
+  if (B <= 0 || N <= 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0) return ATTN_EINVAL;
+  const long long lim = 1ll << 31;
+  if ((long long)max_pages * page_size >= lim || (long long)num_pages * page_size >= lim ||
+      (long long)B * N >= lim)
+    return ATTN_EUNSUPPORTED;
+  if (!aligned4(old_lens) || !aligned4(new_lens) || !aligned4(block_table) ||
+      !aligned4(free_pages) || !aligned4(state_in) || !aligned4(state_out) || !aligned4(index) ||
+      !aligned4(slots))
+    return ATTN_EALIGN;
+  if (ranges_meet(state_in, 8, state_out, 8)) return ATTN_EINVAL;   // read by every CTA, written by one
+  return launch_paged_plan(old_lens, new_lens, block_table, free_pages, state_in, state_out, index,
+                           slots, B, N, max_pages, page_size, num_pages,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int kv_append(const void* q, const void* k, const void* v, const int64_t* strides,
+              const int32_t* positions, float rope_base, int rope_pairing, void* q_out,
+              void* k_out, const int32_t* slots, void* k_cache, void* v_cache, int B, int Hq,
+              int Hkv, int N, int d, int page_size, int num_pages, void* stream) {
+  if (!k || B <= 0 || Hq < 0 || Hkv <= 0 || N <= 0 || d <= 0) return ATTN_EINVAL;
+  if ((q == nullptr) != (Hq == 0) || (q == nullptr) != (q_out == nullptr)) return ATTN_EINVAL;
+  const bool store = slots != nullptr;
+  if (store != (v != nullptr) || store != (k_cache != nullptr) || store != (v_cache != nullptr))
+    return ATTN_EINVAL;
+  if (store ? (page_size <= 0 || num_pages <= 0) : k_out == nullptr) return ATTN_EINVAL;
+  if (!positions && (q || k_out)) return ATTN_EINVAL;
+  if (positions && (!std::isfinite(rope_base) || !(rope_base > 0.f))) return ATTN_EINVAL;
+  if (rope_pairing != 0 && rope_pairing != 1) return ATTN_EINVAL;
+  if (d != 64 && d != 128) return ATTN_EUNSUPPORTED;
+  const long long lim = 1ll << 31;
+  if ((long long)B * N >= lim || (long long)Hq + 2ll * Hkv >= 65536 ||
+      (long long)B * N * (Hq > Hkv ? Hq : Hkv) >= lim)
+    return ATTN_EUNSUPPORTED;
+  if (store && ((long long)num_pages * page_size >= lim ||
+                (long long)num_pages * page_size * Hkv >= lim))
+    return ATTN_EUNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(positions) || !aligned4(slots))
+    return ATTN_EALIGN;
+  const int heads[3] = {Hq, Hkv, Hkv};
+  int64_t s[9];
+  for (int i = 0; i < 3; ++i) {
+    const int64_t full[3] = {(int64_t)heads[i] * N * d, (int64_t)N * d, d};
+    const int size[3] = {B, heads[i], N};
+    for (int j = 0; j < 3; ++j) {
+      // (a stride over one element is never used)
+      s[3 * i + j] = size[j] <= 1 ? 0 : (strides ? strides[3 * i + j] : full[j]);
+      if (s[3 * i + j] % 8 != 0) return ATTN_EALIGN;
+      if (s[3 * i + j] < 0) return ATTN_EINVAL;
+    }
+  }
+  // an output may be its own input, laid out the same, and meet no other
+  const void* in[3] = {q, k, v};
+  void* out[4] = {q_out, k_out, k_cache, v_cache};
+  const size_t row = (size_t)d * 2, cache = store ? (size_t)num_pages * Hkv * page_size * row : 0;
+  const size_t out_n[4] = {(size_t)B * Hq * N * row, (size_t)B * Hkv * N * row, cache, cache};
+  for (int o = 0; o < 4; ++o) {
+    if (!out[o]) continue;
+    for (int p = o + 1; p < 4; ++p)
+      if (out[p] && ranges_meet(out[o], out_n[o], out[p], out_n[p])) return ATTN_EINVAL;
+    for (int i = 0; i < 3; ++i) {
+      if (!in[i]) continue;
+      if (o == i && out[o] == in[i] && rows_contiguous(s + 3 * i, B, heads[i], N, d)) continue;
+      // smallest byte range that holds the input's rows: interleaved views of
+      // one buffer, as of a fused projection, meet no separate output
+      const size_t n = ((size_t)s[3 * i] * (B - 1) + (size_t)s[3 * i + 1] * (heads[i] - 1) +
+                        (size_t)s[3 * i + 2] * (N - 1)) * 2 + row;
+      if (ranges_meet(out[o], out_n[o], in[i], n)) return ATTN_EINVAL;
+    }
+  }
+  return launch_kv_append(q, k, v, s, positions, rope_base, rope_pairing, q_out, k_out, slots,
+                          k_cache, v_cache, B, Hq, Hkv, N, d, page_size, num_pages,
+                          static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_tree_workspace_size(int B, int Hq, int Hkv, int Nq, int d) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || Hq % Hkv != 0 || !tree_supported(B, Nq, d))
+    return 0;
+  const int sms = current_sms();
+  if (sms <= 0) return 0;
+  return tree_workspace_bytes(B, Hq, Hkv, Nq, d, sms);
+}
+
+int attn_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_table, int max_pages, int page_size, int num_pages,
+                  const void* k_new, const void* v_new, const int32_t* parents,
+                  const int32_t* new_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                  int Nk, int d, float scale, const int32_t* key_lens, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (!k_new || !v_new || !parents) return ATTN_EINVAL;
+  if (block_table) {
+    if (!key_lens || max_pages <= 0 || num_pages <= 0 || page_size <= 0 || Nk != 0)
+      return ATTN_EINVAL;
+    if ((long long)max_pages * page_size >= (1ll << 31)) return ATTN_EUNSUPPORTED;
+    Nk = max_pages * page_size;
+  } else if (max_pages != 0 || page_size != 0 || num_pages != 0) {
+    return ATTN_EINVAL;
+  }
+  // (the capacity of a paged sequence does not bound the cache's rows)
+  int rc = check_common(q, k_cache, v_cache, o, B, Hq, Hkv, Nq, block_table ? 1 : Nk, d, 0, scale);
+  if (rc != ATTN_OK) return rc;
+  if (!tree_supported(B, Nq, d)) return ATTN_EUNSUPPORTED;
+  if (block_table) {
+    if (page_size % 8 != 0 || 128 % page_size != 0) return ATTN_EUNSUPPORTED;
+    if ((long long)num_pages * Hkv * page_size >= (1ll << 31)) return ATTN_EUNSUPPORTED;
+  }
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(lse) || !aligned4(block_table) ||
+      !aligned4(parents) || !aligned4(new_lens) || !aligned4(key_lens))
+    return ATTN_EALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return ATTN_ECUDA;
+  if (!workspace || workspace_bytes < tree_workspace_bytes(B, Hq, Hkv, Nq, d, sms))
+    return ATTN_EWORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_EALIGN;
+  TreeArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kc = static_cast<const __nv_bfloat16*>(k_cache);
+  a.vc = static_cast<const __nv_bfloat16*>(v_cache);
+  a.kn = static_cast<const __nv_bfloat16*>(k_new);
+  a.vn = static_cast<const __nv_bfloat16*>(v_new);
+  a.block_table = block_table;
+  a.key_lens = key_lens;
+  a.parents = parents;
+  a.new_lens = new_lens;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.Nq = Nq; a.Nk = Nk;
+  a.max_pages = max_pages; a.page_size = page_size; a.num_pages = num_pages;
+  a.scale_log2 = scale * kLog2e;
+  return launch_tree(a, d, workspace, sms, static_cast<cudaStream_t>(stream));
 }
 
 int attn_prefill_tile_shape(int d, int* Br, int* Bc) {

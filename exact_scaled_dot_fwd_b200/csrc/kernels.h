@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -110,5 +111,38 @@ int launch_rope(const void* x_in, void* x_out, int B, int H, int N, int d, float
                 int pos_offset, int pairing, cudaStream_t st);
 // (cos, sin) of positions pos_offset .. pos_offset + N - 1: tab[t * d/2 + i]
 int launch_rope_table(float2* tab, int N, int d, float base, int pos_offset, cudaStream_t st);
+
+// ---- serving over a cache (contracts in attn.h)
+int launch_paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t* block_table,
+                      int32_t* free_pages, const int32_t* state_in, int32_t* state_out,
+                      const int32_t* index, int32_t* slots, int B, int N, int max_pages,
+                      int page_size, int num_pages, cudaStream_t st);
+// strides: {batch, head, token} of q, k, v in elements
+int launch_kv_append(const void* q, const void* k, const void* v, const int64_t* strides,
+                     const int32_t* positions, float rope_base, int rope_pairing, void* q_out,
+                     void* k_out, const int32_t* slots, void* k_cache, void* v_cache, int B,
+                     int Hq, int Hkv, int N, int d, int page_size, int num_pages,
+                     cudaStream_t st);
+
+// ---- attention for a tree of drafted tokens over a cache
+struct TreeArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kc;        // cache: paged if block_table, else [B, Hkv, Nk, d]
+  const __nv_bfloat16* vc;
+  const __nv_bfloat16* kn;        // drafted keys and values [B, Hkv, Nq, d]
+  const __nv_bfloat16* vn;
+  const int32_t* block_table;
+  const int32_t* key_lens;
+  const int32_t* parents;
+  const int32_t* new_lens;
+  __nv_bfloat16* o;
+  float* lse;
+  int B, Hq, Hkv, Nq, Nk;         // Nk: capacity of a sequence's cache
+  int max_pages, page_size, num_pages;
+  float scale_log2;
+};
+bool tree_supported(int B, int Nq, int d);
+size_t tree_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int num_sms);
+int launch_tree(const TreeArgs& a, int d, void* workspace, int num_sms, cudaStream_t st);
 
 }  // namespace attn

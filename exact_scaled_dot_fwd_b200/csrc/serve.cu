@@ -1,0 +1,390 @@
+// serve.cu -- the passes around attention over a paged cache: the page plan
+// of a step (block tables and slot maps from request lengths) and the append
+// of new keys and values, rotated at their own positions.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "rope_math.cuh"
+#include "tile_plan.cuh"
+
+namespace attn {
+
+// ------------------------------------------------------------------ page plan
+//
+// With h(x) = ceil(x / page_size), sequence b takes a_b = max(0, h(new) -
+// h(old)) pages and gives back r_b = max(0, h(old) - h(new)).  Its pages are
+// the queue's entries A_b .. A_b + a_b - 1 with A_b = sum_{c < b} a_c (r
+// likewise at the tail), so every entry and slot has a closed form once the
+// two prefix sums are known, and nothing has to be exchanged between CTAs:
+// each one sums the lengths below its own sequences again (8 bytes per
+// sequence, out of L2) instead of waiting for a scan kernel.
+//
+// Bound by launch latency: the whole step is a few KB to a few MB.
+
+namespace {
+constexpr int kPlanThreads = 256;
+constexpr int kPlanMaxS = 64;      // sequences per CTA
+constexpr int kPlanItems = 1024;   // slots per CTA, about
+}  // namespace
+
+struct PlanArgs {
+  const int32_t* old_lens;
+  const int32_t* new_lens;
+  int32_t* table;
+  int32_t* ring;
+  const int32_t* state_in;
+  int32_t* state_out;
+  const int32_t* index;
+  int32_t* slots;
+  int B, N, max_pages, page_size, num_pages;
+  int S;        // sequences per CTA
+  int chunks;   // CTAs per sequence group (S == 1 when above 1)
+};
+
+struct PlanSeq {
+  int o, n;      // old and new length
+  int ho, hn;    // pages held before and after
+};
+
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int b) {
+  PlanSeq s;
+  const int cap = a.max_pages * a.page_size;
+  s.o = clamp_len(a.old_lens[b], cap);
+  s.n = clamp_len(a.new_lens[b], cap);
+  s.ho = (int)(((long long)s.o + a.page_size - 1) / a.page_size);
+  s.hn = (int)(((long long)s.n + a.page_size - 1) / a.page_size);
+  return s;
+}
+
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
+  __shared__ long long s_red[4][kPlanThreads / 32];
+  __shared__ PlanSeq s_seq[kPlanMaxS];
+  __shared__ long long s_take[kPlanMaxS], s_give[kPlanMaxS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int grp = blockIdx.x / a.chunks, chunk = blockIdx.x - grp * a.chunks;
+  const int b0 = grp * a.S;
+  const int S = a.B - b0 < a.S ? a.B - b0 : a.S;
+  const bool last = blockIdx.x == 0;   // this CTA also writes the queue's new state
+
+  // pages taken and given back by the sequences below b0 (and by all)
+  long long tk = 0, gv = 0, tk_all = 0, gv_all = 0;
+  const int upto = last ? a.B : b0;
+  for (int b = tid; b < upto; b += kPlanThreads) {
+    const PlanSeq s = plan_seq(a, b);
+    const int t = s.hn > s.ho ? s.hn - s.ho : 0, g = s.ho > s.hn ? s.ho - s.hn : 0;
+    if (b < b0) { tk += t; gv += g; }
+    tk_all += t;
+    gv_all += g;
+  }
+  tk = warp_sum(tk); gv = warp_sum(gv); tk_all = warp_sum(tk_all); gv_all = warp_sum(gv_all);
+  if (lane == 0) { s_red[0][warp] = tk; s_red[1][warp] = gv; s_red[2][warp] = tk_all; s_red[3][warp] = gv_all; }
+  if (tid < S) s_seq[tid] = plan_seq(a, b0 + tid);
+  __syncthreads();
+  if (warp == 0) {
+    long long t0 = 0, g0 = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) { t0 += s_red[0][w]; g0 += s_red[1][w]; }
+    // exclusive scan over this CTA's sequences, 32 at a time
+    for (int base = 0; base < S; base += 32) {
+      const int i = base + lane;
+      long long t = 0, g = 0;
+      if (i < S) {
+        const PlanSeq s = s_seq[i];
+        t = s.hn > s.ho ? s.hn - s.ho : 0;
+        g = s.ho > s.hn ? s.ho - s.hn : 0;
+      }
+      long long xt = t, xg = g;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long yt = __shfl_up_sync(0xffffffffu, xt, o);
+        const long long yg = __shfl_up_sync(0xffffffffu, xg, o);
+        if (lane >= o) { xt += yt; xg += yg; }
+      }
+      if (i < S) { s_take[i] = t0 + xt - t; s_give[i] = g0 + xg - g; }
+      t0 += __shfl_sync(0xffffffffu, xt, 31);
+      g0 += __shfl_sync(0xffffffffu, xg, 31);
+    }
+  }
+  __syncthreads();
+
+  // the queue; a state from elsewhere cannot lead outside the ring
+  const int P = a.num_pages;
+  int head = a.state_in[0] % P;
+  if (head < 0) head += P;
+  const int count = clamp_len(a.state_in[1], P);
+  bool bad = false;
+  // m-th page taken, or -1
+  auto taken = [&](long long m) -> int {
+    if (m >= count) return -1;
+    return a.ring[(int)((head + m) % P)];
+  };
+
+  if (last && tid == 0) {
+    long long t = 0, g = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) { t += s_red[2][w]; g += s_red[3][w]; }
+    const long long served = t < count ? t : count;
+    const long long room = P - count;
+    const long long back = g < room ? g : room;
+    a.state_out[0] = (int)((head + served) % P);
+    a.state_out[1] = (int)(count - served + back);
+    if (t > count || g > room) bad = true;
+  }
+
+  // table entries taken, ring entries given back: a warp per sequence (all
+  // warps and chunks on the one sequence of a long row)
+  const int w0 = a.S > 1 ? warp : 0, wn = a.S > 1 ? kPlanThreads / 32 : 1;
+  const int l0 = a.S > 1 ? lane : chunk * kPlanThreads + tid;
+  const int ln = a.S > 1 ? 32 : a.chunks * kPlanThreads;
+  for (int s = w0; s < S; s += wn) {
+    const PlanSeq q = s_seq[s];
+    int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages;
+    for (int j = q.ho + l0; j < q.hn; j += ln) row[j] = taken(s_take[s] + (j - q.ho));
+    for (int j = q.hn + l0; j < q.ho; j += ln) {
+      const long long m = s_give[s] + (j - q.hn);
+      if (m < P - count) a.ring[(int)(((long long)head + count + m) % P)] = row[j];
+    }
+  }
+
+  // slots
+  const int i0 = a.S > 1 ? 0 : chunk * kPlanItems;
+  int per = a.N - i0;
+  if (a.S == 1 && per > kPlanItems) per = kPlanItems;
+  for (int it = tid; it < S * per; it += kPlanThreads) {
+    const int s = it / per, i = i0 + (it - s * per);
+    const PlanSeq q = s_seq[s];
+    const size_t at = (size_t)(b0 + s) * a.N + i;
+    const int t = a.index ? a.index[at] : i;
+    int slot = -1;
+    if (t >= 0 && t < q.n - q.o) {
+      const int p = q.o + t;
+      const int j = p / a.page_size;
+      const int page = j < q.ho ? a.table[(size_t)(b0 + s) * a.max_pages + j]
+                                : taken(s_take[s] + (j - q.ho));
+      if ((unsigned)page < (unsigned)P) slot = page * a.page_size + (p - j * a.page_size);
+      else bad = true;
+    }
+    a.slots[at] = slot;
+  }
+  if (bad) atomicExch(&g_device_status, (int)ATTN_ERANGE);
+}
+
+int launch_paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t* block_table,
+                      int32_t* free_pages, const int32_t* state_in, int32_t* state_out,
+                      const int32_t* index, int32_t* slots, int B, int N, int max_pages,
+                      int page_size, int num_pages, cudaStream_t st) {
+  PlanArgs a;
+  a.old_lens = old_lens; a.new_lens = new_lens; a.table = block_table; a.ring = free_pages;
+  a.state_in = state_in; a.state_out = state_out; a.index = index; a.slots = slots;
+  a.B = B; a.N = N; a.max_pages = max_pages; a.page_size = page_size; a.num_pages = num_pages;
+  a.S = kPlanItems / N;
+  if (a.S < 1) a.S = 1;
+  if (a.S > kPlanMaxS) a.S = kPlanMaxS;
+  a.chunks = a.S > 1 ? 1 : (N + kPlanItems - 1) / kPlanItems;
+  const long long grid = (long long)((B + a.S - 1) / a.S) * a.chunks;
+  paged_plan_kernel<<<(unsigned)grid, kPlanThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ECUDA;
+}
+
+// ------------------------------------------------------------------ append
+//
+// A CTA owns a tile of tokens for a slab of the head rows [q heads | k heads |
+// v heads].  It builds the (cos, sin) of its tokens in shared memory (the
+// frequency of a thread's pairs is raised once, the angle is formed and
+// reduced in 64 bits as in rope_apply, so the results are the same bits) and
+// a list of the tokens that have a slot, then streams the rows: a thread
+// takes 32 bytes of a row -- the two 16-byte chunks that hold its 8 pairs --
+// and writes them to q_out / k_out and to the cache.  Bound by HBM for
+// prompts, by latency for a decode step.
+
+namespace {
+constexpr int kAppThreads = 256;
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+}  // namespace
+
+struct AppendArgs {
+  const __nv_bfloat16* x[3];     // q, k, v
+  long long sb[3], sh[3], st[3]; // strides of batch, head, token in elements
+  const int32_t* positions;
+  const int32_t* slots;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* kc;
+  __nv_bfloat16* vc;
+  int B, Hq, Hkv, N, page_size, num_pages;
+  int heads;                     // Hq + Hkv (+ Hkv with v)
+  int slabs;
+  double base;
+};
+
+template <int D, bool kRope, bool kAdjacent, int TT>
+__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(AppendArgs a) {
+  constexpr int kHalf = D / 2;
+  constexpr int kChunks = D / 16;     // 32-byte items of a row
+  __shared__ float2 tab[kRope ? TT * kHalf : 1];
+  __shared__ int s_slot[TT], s_list[TT];
+  __shared__ int s_kept;
+  const int tid = threadIdx.x;
+  const long long T = (long long)a.B * a.N;
+  const long long t0 = (long long)blockIdx.x * TT;
+  const int nt = T - t0 < TT ? (int)(T - t0) : TT;
+  if (tid < 32) {
+    // slots of the tile's tokens, and the list of those that are stored
+    const long long rows = (long long)a.num_pages * a.page_size;
+    int s = -1;
+    if (a.slots && tid < nt) {
+      s = a.slots[t0 + tid];
+      if (s >= rows) {
+        s = -1;
+        atomicExch(&g_device_status, (int)ATTN_ERANGE);
+      }
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, s >= 0);
+    if (tid < TT) s_slot[tid] = s;
+    if (s >= 0) s_list[__popc(m & ((1u << tid) - 1))] = tid;
+    if (tid == 0) s_kept = __popc(m);
+  }
+  if constexpr (kRope) {
+    const int i = tid % kHalf;
+    const double theta = pow(a.base, -2.0 * (double)i / (double)D);
+    for (int t = tid / kHalf; t < nt; t += kAppThreads / kHalf) {
+      double s, c;
+      sincos((double)a.positions[t0 + t] * theta, &s, &c);
+      tab[t * kHalf + i] = make_float2((float)c, (float)s);
+    }
+  }
+  __syncthreads();
+  const int kept = s_kept;
+  const int h0 = (int)((long long)a.heads * blockIdx.y / a.slabs);
+  const int h1 = (int)((long long)a.heads * (blockIdx.y + 1) / a.slabs);
+
+  for (int part = 0; part < 3; ++part) {
+    // head rows of this part in the slab
+    const int p0 = part == 0 ? 0 : (part == 1 ? a.Hq : a.Hq + a.Hkv);
+    const int p1 = part == 0 ? a.Hq : (part == 1 ? a.Hq + a.Hkv : a.heads);
+    const int f = h0 > p0 ? h0 : p0, e = h1 < p1 ? h1 : p1;
+    if (f >= e) continue;
+    __nv_bfloat16* out = part == 0 ? a.q_out : (part == 1 ? a.k_out : nullptr);
+    __nv_bfloat16* cache = part == 0 ? nullptr : (part == 1 ? a.kc : a.vc);
+    const int H = part == 0 ? a.Hq : a.Hkv;
+    // without a copy outside the cache only the stored tokens matter
+    const int n = out ? nt : kept;
+    const bool rot = kRope && part < 2;
+    // chunks of an item: pairs (i, i + D/2) sit in chunk c of each half,
+    // adjacent pairs and plain copies in two neighbouring chunks
+    const bool halves = rot && !kAdjacent;
+    for (int it = tid; it < (e - f) * n * kChunks; it += kAppThreads) {
+      const int c = it % kChunks;
+      const int r = it / kChunks;
+      const int li = r % n;
+      const int h = f - p0 + r / n;
+      const int t = out ? li : s_list[li];
+      const long long tok = t0 + t;
+      const int b = (int)(tok / a.N), i = (int)(tok - (long long)b * a.N);
+      const int e0 = halves ? 8 * c : 16 * c, e1 = halves ? kHalf + 8 * c : 16 * c + 8;
+      const __nv_bfloat16* src =
+          a.x[part] + b * a.sb[part] + h * a.sh[part] + i * a.st[part];
+      uint4 va = *reinterpret_cast<const uint4*>(src + e0);
+      uint4 vb = *reinterpret_cast<const uint4*>(src + e1);
+      if (rot) {
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+        uint32_t oa[4], ob[4];
+        const float2* cs = tab + t * kHalf + 8 * c;
+        if constexpr (kAdjacent) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float r0, r1;
+            rope_rotate(lo_bf16(wa[k]), hi_bf16(wa[k]), cs[k], r0, r1);
+            oa[k] = pack_bf16x2(r0, r1);
+            rope_rotate(lo_bf16(wb[k]), hi_bf16(wb[k]), cs[4 + k], r0, r1);
+            ob[k] = pack_bf16x2(r0, r1);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float ra0, rb0, ra1, rb1;
+            rope_rotate(lo_bf16(wa[k]), lo_bf16(wb[k]), cs[2 * k], ra0, rb0);
+            rope_rotate(hi_bf16(wa[k]), hi_bf16(wb[k]), cs[2 * k + 1], ra1, rb1);
+            oa[k] = pack_bf16x2(ra0, ra1);
+            ob[k] = pack_bf16x2(rb0, rb1);
+          }
+        }
+        va = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+        vb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+      }
+      if (out) {
+        __nv_bfloat16* o = out + (((size_t)b * H + h) * a.N + i) * D;
+        *reinterpret_cast<uint4*>(o + e0) = va;
+        *reinterpret_cast<uint4*>(o + e1) = vb;
+      }
+      const int slot = s_slot[t];
+      if (cache && slot >= 0) {
+        const int page = slot / a.page_size;
+        __nv_bfloat16* o =
+            cache + (((size_t)page * a.Hkv + h) * a.page_size + (slot - page * a.page_size)) * D;
+        *reinterpret_cast<uint4*>(o + e0) = va;
+        *reinterpret_cast<uint4*>(o + e1) = vb;
+      }
+    }
+  }
+}
+
+namespace {
+template <int D, bool kRope, bool kAdjacent>
+int launch_append_t(AppendArgs a, cudaStream_t st) {
+  const long long T = (long long)a.B * a.N;
+  // a tile of 32 tokens fills the machine from some 10k tokens on; below
+  // that smaller tiles and slabs of heads spread the rows over the SMs
+  const bool small = T <= 1024;
+  const long long tiles = (T + (small ? 4 : 32) - 1) / (small ? 4 : 32);
+  long long slabs = (296 + tiles - 1) / tiles;
+  if (slabs > a.heads) slabs = a.heads;
+  a.slabs = (int)slabs;
+  const dim3 grid((unsigned)tiles, (unsigned)slabs);
+  if (small) kv_append_kernel<D, kRope, kAdjacent, 4><<<grid, kAppThreads, 0, st>>>(a);
+  else kv_append_kernel<D, kRope, kAdjacent, 32><<<grid, kAppThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ECUDA;
+}
+}  // namespace
+
+int launch_kv_append(const void* q, const void* k, const void* v, const int64_t* strides,
+                     const int32_t* positions, float rope_base, int rope_pairing, void* q_out,
+                     void* k_out, const int32_t* slots, void* k_cache, void* v_cache, int B,
+                     int Hq, int Hkv, int N, int d, int page_size, int num_pages,
+                     cudaStream_t st) {
+  AppendArgs a;
+  const void* x[3] = {q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    a.x[i] = static_cast<const __nv_bfloat16*>(x[i]);
+    a.sb[i] = strides[3 * i];
+    a.sh[i] = strides[3 * i + 1];
+    a.st[i] = strides[3 * i + 2];
+  }
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.kc = static_cast<__nv_bfloat16*>(k_cache);
+  a.vc = static_cast<__nv_bfloat16*>(v_cache);
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.N = N;
+  a.page_size = page_size; a.num_pages = num_pages;
+  a.heads = Hq + Hkv + (slots ? Hkv : 0);
+  a.base = (double)rope_base;
+  if (d == 128) {
+    if (!positions) return launch_append_t<128, false, false>(a, st);
+    return rope_pairing ? launch_append_t<128, true, true>(a, st)
+                        : launch_append_t<128, true, false>(a, st);
+  }
+  if (!positions) return launch_append_t<64, false, false>(a, st);
+  return rope_pairing ? launch_append_t<64, true, true>(a, st)
+                      : launch_append_t<64, true, false>(a, st);
+}
+
+}  // namespace attn

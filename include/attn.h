@@ -59,7 +59,7 @@ typedef enum {
   ATTN_EWORKSPACE = 4,    /* workspace missing or smaller than attn_workspace_size() */
   ATTN_ECUDA = 5,         /* a CUDA runtime / driver call failed (launch, attribute) */
   ATTN_ETIMEOUT = 6,      /* a kernel gave up waiting on a barrier (device status) */
-  ATTN_ERANGE = 7         /* a kernel met an out-of-range block-table entry (device status) */
+  ATTN_ERANGE = 7         /* a kernel met an out-of-range table entry, slot or parent (device status) */
 } attn_status;
 
 /* Exact attention forward.  Dispatch: calls with at most 64 query rows per kv
@@ -303,10 +303,127 @@ ATTN_API int attn_fwd_decode_static(const void* q, const void* k, const void* v,
 /* Size in bytes of the device array attn_fwd_decode_static works in. */
 ATTN_API size_t attn_decode_static_max_bytes(void);
 
+/* ---- Serving over a cache: page plan, append, attention for a draft tree.
+ *
+ * One step of a server that drafts tokens runs: kv_append (rotate the drafted
+ * nodes' q and k at their own positions), attn_fwd_tree (attend to the cache
+ * and to the tree), then, for the nodes that were accepted, paged_plan (pages
+ * and slots) and kv_append (store).  A decode or prompt step runs paged_plan
+ * and kv_append on its new tokens, then attn_fwd_paged.  Drafted keys are in
+ * the cache only once accepted, so nothing is moved or rolled back. */
+
+/* Block tables and slot maps from request lengths ("Attention mechanisms
+ * ...", section 20: block table and free list of a paged cache).  Sequence b
+ * goes from old_lens[b] to new_lens[b] tokens (both clamped to [0, max_pages
+ * * page_size]); with h(x) = ceil(x / page_size) it
+ *   - takes pages for block_table[b][h(old) .. h(new)) when it grows, and
+ *   - gives the pages block_table[b][h(new) .. h(old)) back when it shrinks
+ *     (new_lens[b] = 0: a finished request).
+ * Free pages form a queue in the ring free_pages[num_pages]: state_in =
+ * {head, count}; pages are taken from the head in order of (b, entry) and
+ * given back at the tail in the same order, so what is given back can be
+ * taken from the next call on.  state_out = {head, count} afterwards.
+ *   slots[b * N + i] is the cache slot, page * page_size + row, of the
+ * sequence's new token t = index ? index[b * N + i] : i, i.e. of position
+ * old_lens[b] + t, if 0 <= t < new_lens[b] - old_lens[b], else -1.  (index
+ * maps the nodes of a draft tree to their place on the accepted path, -1 for
+ * a rejected node.)
+ *   old_lens, new_lens: DEVICE int32 [B]; block_table: DEVICE int32 [B,
+ * max_pages], entries outside the ranges above are left as they were;
+ * free_pages: DEVICE int32 [num_pages]; state_in, state_out: DEVICE int32
+ * [2], not the same buffer; index: DEVICE int32 [B, N] or NULL; slots:
+ * DEVICE int32 [B, N].  4-byte alignment is enough.
+ *   If the queue runs empty, the entries that got no page become -1, their
+ * tokens get slot -1, state_out holds count 0 plus the pages given back, and
+ * the device status word records ATTN_ERANGE; so it does for a table entry
+ * outside [0, num_pages) that a slot would need (slot -1) and for pages
+ * given back beyond the ring's room (dropped).  No value makes the kernel
+ * access memory outside the buffers.
+ *   A page belongs to one sequence: the call does not count references.
+ * Errors: ATTN_EINVAL (null pointers, sizes <= 0, state_in == state_out),
+ * ATTN_EUNSUPPORTED (max_pages * page_size, num_pages * page_size or B * N
+ * not below 2^31), ATTN_EALIGN, ATTN_ECUDA. */
+ATTN_API int paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t* block_table,
+                        int32_t* free_pages, const int32_t* state_in, int32_t* state_out,
+                        const int32_t* index, int32_t* slots, int B, int N, int max_pages,
+                        int page_size, int num_pages, void* stream);
+
+/* Rotates a step's queries and keys at each token's own position and stores
+ * the keys and values in the cache, in one pass.
+ *   q bf16 [B, Hq, N, d] (or NULL with Hq = 0), k, v bf16 [B, Hkv, N, d]:
+ * DEVICE, any strides over (b, head, token) that are multiples of 8 elements
+ * with d contiguous -- views of a fused projection's output.  strides: HOST
+ * int64 [9] = {b, head, token} of q, k, v in elements, or NULL: all
+ * contiguous.
+ *   positions: DEVICE int32 [B, N] or NULL (nothing is rotated; then q and
+ * k_out are NULL).  Row (b, t) of q and k is rotated at positions[b * N + t]
+ * with rope_apply's frequencies, pairing and arithmetic (bit for bit).
+ *   q_out bf16 [B, Hq, N, d], k_out bf16 [B, Hkv, N, d], contiguous: the
+ * rotated q (required with q) and k (or NULL).  q_out == q and k_out == k
+ * are allowed for contiguous inputs; other overlaps are not.
+ *   slots: DEVICE int32 [B, N] or NULL (nothing is stored; then v, k_cache
+ * and v_cache are NULL and k_out is required): token (b, t) goes to row s %
+ * page_size of page s / page_size of k_cache, v_cache bf16 [num_pages, Hkv,
+ * page_size, d]; s < 0: not stored; s >= num_pages * page_size: not stored,
+ * and the device status word records ATTN_ERANGE.  Slots are distinct: of two
+ * tokens with one slot either may be stored, or parts of both.  A contiguous
+ * cache [B, Hkv, Nk, d] is B pages of Nk rows (slot b * Nk + position);
+ * page_size is any positive number here.  Other cache rows are left as they
+ * were.
+ * Errors: ATTN_EINVAL (null / missing pairs above, sizes, base, pairing,
+ * overlap), ATTN_EUNSUPPORTED (d not 64 or 128, sizes of 2^31 rows or more),
+ * ATTN_EALIGN (pointers of bf16 tensors 16 bytes, strides of 8 elements),
+ * ATTN_ECUDA. */
+ATTN_API int kv_append(const void* q, const void* k, const void* v, const int64_t* strides,
+                       const int32_t* positions, float rope_base, int rope_pairing,
+                       void* q_out, void* k_out, const int32_t* slots, void* k_cache,
+                       void* v_cache, int B, int Hq, int Hkv, int N, int d, int page_size,
+                       int num_pages, void* stream);
+
+/* Attention for a tree of drafted tokens over a cache (draft verification;
+ * "Coding interview (14)", self-test 5 is the chain).  Sequence b has
+ * key_lens[b] cached keys and new_lens[b] drafted nodes (clamped to [0, Nk]
+ * and [0, Nq]); node i < new_lens[b] sees every cached key, itself and its
+ * ancestors: parents[b * Nq + i] is the node it follows, or -1 for a child of
+ * the last cached token.  Parents come before their children (parent < i); a
+ * value outside [-1, i) is taken as -1 and the device status word records
+ * ATTN_ERANGE.
+ *     O = softmax(Q K^T * scale) V over the visible keys, lse as attn_fwd
+ *   Rows i >= new_lens[b] get O = 0 and lse = -inf.
+ *   q, o bf16 [B, Hq, Nq, d]; lse fp32 [B, Hq, Nq] or NULL; k_new, v_new
+ * bf16 [B, Hkv, Nq, d]: the drafted nodes' keys (rotated at their positions)
+ * and values, not stored in the cache; parents int32 [B, Nq]; new_lens int32
+ * [B] or NULL (= Nq).  All DEVICE.
+ *   block_table != NULL: a paged cache as attn_fwd_paged's (k_cache, v_cache
+ * bf16 [num_pages, Hkv, page_size, d], block_table int32 [B, max_pages],
+ * key_lens required; Nk is max_pages * page_size and the argument is 0);
+ * page_size 8, 16, 32, 64 or 128, for both d; entries outside [0, num_pages)
+ * are treated as there.
+ * block_table == NULL: a contiguous cache [B, Hkv, Nk, d], key_lens NULL =
+ * Nk; max_pages, page_size and num_pages are 0.
+ *   Cache rows at or beyond key_lens[b], and drafted rows at or beyond
+ * new_lens[b], may hold anything, NaN included.
+ *   Workspace: attn_tree_workspace_size(...) bytes, as for attn_fwd_ws.
+ * Errors: ATTN_EINVAL, ATTN_EUNSUPPORTED (d not 64 or 128, Nq > 1024, B >
+ * 2048, page_size, sizes of 2^31 rows or more), ATTN_EALIGN,
+ * ATTN_EWORKSPACE, ATTN_ECUDA. */
+ATTN_API int attn_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_table, int max_pages, int page_size,
+                           int num_pages, const void* k_new, const void* v_new,
+                           const int32_t* parents, const int32_t* new_lens, void* o,
+                           float* lse, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                           float scale, const int32_t* key_lens, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_fwd_tree needs for these sizes on the current
+ * device (0 for invalid sizes). */
+ATTN_API size_t attn_tree_workspace_size(int B, int Hq, int Hkv, int Nq, int d);
+
 /* Synchronises `stream`, then returns the device status word of the current
  * device: ATTN_ETIMEOUT if a kernel of this library gave up on a barrier
- * wait, ATTN_ERANGE if a paged decode met an out-of-range block-table entry
- * (the last such event since the last reset), else ATTN_OK (ATTN_ECUDA if
+ * wait, ATTN_ERANGE if one met an out-of-range block-table entry, slot or
+ * parent, or an empty free-page queue (the last such event since the last
+ * reset), else ATTN_OK (ATTN_ECUDA if
  * the synchronisation failed).  reset != 0 clears the word. */
 ATTN_API int attn_device_status(void* stream, int reset);
 
