@@ -1,99 +1,979 @@
 // tree.cu -- attention for a tree of drafted tokens over a cache: node i of a
 // sequence sees every cached key, itself and its ancestors.
+//
+// The rows of one kv head of one sequence -- its live nodes times the query
+// heads that share the kv head, packed without the padding nodes -- are cut
+// into row groups of up to 256.  A unit is one (sequence, kv head, row
+// group); its keys come in tiles of 128: the cached ones (ceil(L / 128) tiles,
+// whole pages each), then the drafted ones, so only the last cached tile
+// needs a length mask and only the drafted tiles the tree.
+//
+// Work split: all units' tiles are laid end to end with a cost each (Split)
+// and cut evenly over one persistent CTA per SM.  A CTA so gets a run of
+// segments (unit, tiles [j0, j0 + n)).  A unit that lies in one CTA is
+// finished there; one that crosses a cut leaves an fp32 partial result with
+// its log-sum-exp per CTA (at most two a CTA, its first and last segment),
+// and a second kernel joins them.
+//
+// Warp roles (12 warps):
+//   0-3, 4-7   softmax of slot 0 and of slot 1 (a thread owns a TMEM lane)
+//   8          tcgen05.mma issuer, TMEM allocator
+//   9          producer: cuts the segments, loads K and V tiles by TMA
+//   10-11      load Q rows (gathered, so cp.async), clear the dead output rows
+// Steps of a segment alternate between the two slots (TMEM: S0 S1 O0 O1):
+//   row group above 128 rows ("pair"): slot t holds rows 128 t .. of it and
+//     each key tile is taken by both slots in turn;
+//   up to 128 rows: both slots hold the same rows and take every other key
+//     tile, so one tile's softmax runs beside the next one's MMAs; the
+//     slots' (max, sum, O) are joined when the segment ends.
+// The rows are the M side of the MMAs.  With few rows most of M is padding,
+// but a tile's 128x128xD products take about 1000 cycles against the 2700
+// that its 64 KB need from HBM, so it costs nothing until two row tiles are
+// full; a warp without live rows skips its softmax.
+//
+// P goes back to TMEM as bf16 over its S and is the A operand of P V: a
+// weight is off by at most 2^-8, as for every kernel of this library; sums,
+// maxima and O stay in fp32.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 #include "tile_plan.cuh"
 
 namespace attn {
+namespace tr {
 
-// One warp per query row: the lanes hold the row's head dimension, the keys
-// pass one at a time through the running maximum and sum of the softmax.
+constexpr int kTile = 128;        // keys per tile, rows per slot
+constexpr int kThreads = 384;
+constexpr int kMaxB = 2048;
+constexpr int kSegSlots = 4;      // depth of the ring of segments
+constexpr int kSegReaders = 11;   // warps that read it: MMA, 2 Q, 8 softmax
+constexpr float kRescaleLog2 = 8.0f;
+
+// Costs of the work split, in parts of a tile's HBM time: a tile of up to 128
+// rows, one of a pair, and what a unit's start costs.
+constexpr int kCostTile = 5, kCostPair = 8, kCostUnit = 5;
+
 template <int D>
-__global__ void __launch_bounds__(128) tree_rows_kernel(TreeArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.Hq * a.Nq) return;
-  const int i = (int)(row % a.Nq);
-  const int hq = (int)(row / a.Nq % a.Hq), b = (int)(row / a.Nq / a.Hq);
-  const int h = hq / (a.Hq / a.Hkv);
-  const int L = clamp_len(a.key_lens ? a.key_lens[b] : a.Nk, a.Nk);
-  const int n = clamp_len(a.new_lens ? a.new_lens[b] : a.Nq, a.Nq);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[row * D + lane * E + e]) * a.scale_log2;
-    o[e] = 0.f;
-  }
-  auto add = [&](const __nv_bfloat16* kr, const __nv_bfloat16* vr) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(kr[lane * E + e]), s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn), p = exp2_approx(s - mn);
-    l = fmaf(l, f, p);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(p, __bfloat162float(vr[lane * E + e]), o[e] * f);
-    m = mn;
+struct Smem {
+  static constexpr int kBox = kTile * 128;       // 64-column half of a tile
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int NS = D == 128 ? 5 : 10;   // ring of K and V tiles
+  static constexpr int kQ = 0;                   // Q tiles [2]
+  static constexpr int kKV = 2 * kTileBytes;
+  static constexpr int kMl = kKV + NS * kTileBytes;   // float2 [2][128]: (max, sum) of a slot's rows
+  static constexpr int kBar = kMl + 2 * kTile * 8;
+  enum {
+    FULL = 0,
+    EMPTY = FULL + NS,
+    Q_FULL = EMPTY + NS,      // [2], 2 arrivals
+    Q_EMPTY = Q_FULL + 2,     // [2]
+    S_FULL = Q_EMPTY + 2,     // [2]
+    P_FULL = S_FULL + 2,      // [2], 128 arrivals
+    O_FULL = P_FULL + 2,      // [2]
+    SEG_FULL = O_FULL + 2,    // [kSegSlots]
+    SEG_EMPTY = SEG_FULL + kSegSlots,   // [kSegSlots], kSegReaders arrivals
+    MMA_DONE = SEG_EMPTY + kSegSlots,
+    NUM_BARS = MMA_DONE + 1
   };
-  if (i < n) {
-    for (int j = 0; j < L; ++j) {
-      long long r;
-      if (a.block_table) {
-        const int page = a.block_table[(size_t)b * a.max_pages + j / a.page_size];
-        if ((unsigned)page >= (unsigned)a.num_pages) {   // its keys and values read as zeros
-          if (lane == 0) atomicExch(&g_device_status, (int)ATTN_ERANGE);
-          const float mn = fmaxf(m, 0.f);
-          const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-          l = fmaf(l, f, exp2_approx(-mn));
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] *= f;
-          m = mn;
-          continue;
-        }
-        r = ((long long)page * a.Hkv + h) * a.page_size + j % a.page_size;
-      } else {
-        r = ((long long)b * a.Hkv + h) * a.Nk + j;
-      }
-      add(a.kc + r * D, a.vc + r * D);
+  static constexpr int kSeg = kBar + NUM_BARS * 8;   // int [kSegSlots][kSegInts]
+  static constexpr int kSegInts = 8;
+  static constexpr int kScan = kSeg + kSegSlots * kSegInts * 4;   // long long [16]
+  static constexpr int kTmemSlot = kScan + 16 * 8;
+  static constexpr int kAbort = kTmemSlot + 8;
+  static constexpr int kTotal = kAbort + 8;   // (the base is 1024-byte aligned)
+  static_assert(kTotal <= 232448, "shared memory over the 227 KB per-CTA limit");
+};
+
+struct Args {
+  TreeArgs t;
+  float* part_o;      // [2 * grid][RP][D]
+  float* part_lse;    // [2 * grid][RP], log2 units
+  int* meta;          // [grid][8], see the producer
+  int G, RP, grid, oob_row;
+};
+
+// A segment as its readers see it.
+struct Seg {
+  int b, h, rg;       // unit
+  int j0, n;          // key tiles [j0, j0 + n); n = 0 ends the stream
+  int L, nb;          // cached keys, live nodes
+  int flags;          // 1: the CTA's first segment, 2: the whole unit
+  __device__ __forceinline__ int np() const { return (L + kTile - 1) / kTile; }
+};
+
+__device__ __forceinline__ int cached_len(const TreeArgs& t, int b) {
+  return clamp_len(t.key_lens ? t.key_lens[b] : t.Nk, t.Nk);
+}
+__device__ __forceinline__ int live_nodes(const TreeArgs& t, int b) {
+  return clamp_len(t.new_lens ? t.new_lens[b] : t.Nq, t.Nq);
+}
+
+// The units of one sequence and their costs.
+struct Split {
+  int nt;              // tiles of a unit (0: no live node, no unit)
+  int nrg;             // row groups of a kv head
+  int w_last;          // tile cost of the last row group (the others are pairs)
+  long long head;      // cost of a kv head
+  __device__ __forceinline__ Split(int L, int nb, int G) {
+    const int rows = G * nb;
+    nt = nb > 0 ? (L + kTile - 1) / kTile + (nb + kTile - 1) / kTile : 0;
+    nrg = (rows + 2 * kTile - 1) / (2 * kTile);
+    w_last = rows - (nrg - 1) * 2 * kTile > kTile ? kCostPair : kCostTile;
+    head = nb > 0 ? (long long)(nrg - 1) * unit(kCostPair) + unit(w_last) : 0;
+  }
+  __device__ __forceinline__ int weight(int rg) const { return rg < nrg - 1 ? kCostPair : w_last; }
+  __device__ __forceinline__ long long unit(int w) const { return kCostUnit + (long long)nt * w; }
+  // where tile j of a unit starts (the unit's own cost belongs to tile 0)
+  static __device__ __forceinline__ long long tile_at(int j, int w) {
+    return j == 0 ? 0 : kCostUnit + (long long)j * w;
+  }
+  // tiles of a unit that start before x
+  __device__ __forceinline__ int tiles_before(long long x, int w) const {
+    if (x <= 0) return 0;
+    const long long j = (x - kCostUnit + w - 1) / w;   // (truncation: <= 0 below the unit cost)
+    return j < 1 ? 1 : (j > nt ? nt : (int)j);
+  }
+};
+
+// 4D tiled load (no multicast): one page of a paged cache, d = 128.
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+}  // namespace tr
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(tr::kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                   const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn,
+                   tr::Args a) {
+  using namespace tr;
+  using L = Smem<D>;
+  constexpr int NS = L::NS;
+  constexpr uint32_t kIdescS = tc::idesc_bf16(kTile, kTile, false, false);
+  constexpr uint32_t kIdescPV = tc::idesc_bf16(kTile, D, false, true);
+  // no room for aligning by hand: the swizzled tiles rely on the declaration
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  volatile int* segs = reinterpret_cast<volatile int*>(smem + L::kSeg);
+  long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  const TreeArgs& t = a.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if ((smem_u32(smem) & 1023u) != 0) {   // (never seen; nothing below would be in place)
+    atomicExch(&g_device_status, (int)ATTN_ECUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NUM_BARS; ++i) {
+      uint32_t c = 1;
+      if (i == L::P_FULL || i == L::P_FULL + 1) c = 128;
+      if (i == L::Q_FULL || i == L::Q_FULL + 1) c = 2;
+      if (i >= L::SEG_EMPTY && i < L::SEG_EMPTY + kSegSlots) c = kSegReaders;
+      mbar_init(&bars[i], c);
     }
-    for (int j = i; j >= 0;) {
-      const long long r = ((long long)b * a.Hkv + h) * a.Nq + j;
-      add(a.kn + r * D, a.vn + r * D);
-      const int p = a.parents[(size_t)b * a.Nq + j];
-      if (p < -1 || p >= j) {
-        if (lane == 0) atomicExch(&g_device_status, (int)ATTN_ERANGE);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tc::alloc(tmem_slot, 512);
+    tc::relinquish();
+  }
+  // Launched as a programmatic dependent of the previous kernel in the
+  // stream: nothing in global memory is touched before it has completed.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- total cost, and the sequence in which this CTA's share starts: a
+  // thread sums `per` sequences, the block scans the threads' sums
+  const int per = (t.B + kThreads - 1) / kThreads;
+  const int b_lo = threadIdx.x * per < t.B ? threadIdx.x * per : t.B;
+  const int b_hi = b_lo + per < t.B ? b_lo + per : t.B;
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b)
+    mine += (long long)t.Hkv * Split(cached_len(t, b), live_nodes(t, b), a.G).head;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  long long before = 0, T = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    T += scan[w];
+  }
+  const long long start = T * blockIdx.x / a.grid, end = T * (blockIdx.x + 1) / a.grid;
+  long long at = before + incl - mine;
+  if (start < end && at <= start && start < at + mine) {
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long c =
+          (long long)t.Hkv * Split(cached_len(t, b), live_nodes(t, b), a.G).head;
+      if (start < at + c) {
+        scan[12] = b;
+        scan[13] = at;
         break;
       }
-      j = p;
+      at += c;
     }
   }
+  __syncthreads();
+
+  // next segment from the ring; every lane of a reading warp takes part
+  auto next_seg = [&](int& k, Seg& s) -> bool {
+    const int slot = k % kSegSlots;
+    if (!mbar_wait_warp(&bars[L::SEG_FULL + slot], (k / kSegSlots) & 1, abort_flag)) return false;
+    volatile int* p = segs + slot * L::kSegInts;
+    s.b = p[0]; s.h = p[1]; s.rg = p[2]; s.j0 = p[3];
+    s.n = p[4]; s.L = p[5]; s.nb = p[6]; s.flags = p[7];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[L::SEG_EMPTY + slot]);
+    ++k;
+    return s.n > 0;
+  };
+  auto group_rows = [&](const Seg& s) -> int {   // live rows of the segment's row group
+    const int r = a.G * s.nb - s.rg * 2 * kTile;
+    return r < 2 * kTile ? r : 2 * kTile;
+  };
+  // Ring positions of a segment of n tiles that starts at g.  Pair: K0 V0 K1
+  // V1 ..; else K0 K1 V0 K2 V1 ..: the order in which the MMAs use them.
+  auto k_pos = [](int g, int j, bool pair) { return pair ? g + 2 * j : (j == 0 ? g : g + 2 * j - 1); };
+  auto v_pos = [](int g, int j, int n, bool pair) {
+    return pair ? g + 2 * j + 1 : (j < n - 1 ? g + 2 * j + 2 : g + 2 * n - 1);
+  };
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      tma_prefetch_desc(&tkn);
+      tma_prefetch_desc(&tvn);
+    }
+    int k = 0, g = 0;        // segments and ring positions so far
+    int armed = 0;           // ring positions whose barrier was armed (for the drain)
+    bool ok = true;
+    int meta_mid = 0, meta_c1 = -1, meta_slot = 0, meta_b = 0, meta_h = 0, meta_rg = 0;
+    int b = 0, h = 0, rg = 0, j0 = 0, Lb = 0, nb = 0;
+    long long p0 = 0;        // where the current unit starts
+    Split sp(0, 0, 1);
+    bool more = start < end;
+    // first unit with live nodes at or after (b, 0, 0)
+    auto load_seq = [&]() {
+      for (; b < t.B; ++b) {
+        Lb = cached_len(t, b);
+        nb = live_nodes(t, b);
+        sp = Split(Lb, nb, a.G);
+        if (sp.nt > 0) return;
+      }
+    };
+    auto next_unit = [&]() {
+      p0 += sp.unit(sp.weight(rg));
+      j0 = 0;
+      if (++rg == sp.nrg) {
+        rg = 0;
+        if (++h == t.Hkv) {
+          h = 0;
+          ++b;
+          load_seq();
+        }
+      }
+    };
+    if (more) {
+      b = (int)scan[12];
+      load_seq();
+      long long rel = start - scan[13];
+      h = (int)(rel / sp.head);
+      rel -= h * sp.head;
+      rg = (int)(rel / sp.unit(kCostPair));
+      if (rg > sp.nrg - 1) rg = sp.nrg - 1;
+      rel -= rg * sp.unit(kCostPair);
+      p0 = start - rel;
+      j0 = rel == 0 ? 0 : sp.tiles_before(rel, sp.weight(rg));
+      if (j0 == sp.nt) next_unit();
+    }
+    while (ok) {
+      const int w = sp.weight(rg);
+      int n = 0;
+      if (more && b < t.B && p0 + Split::tile_at(j0, w) < end) n = sp.tiles_before(end - p0, w) - j0;
+      const int slot = k % kSegSlots;
+      if (!mbar_wait_warp(&bars[L::SEG_EMPTY + slot], ((k / kSegSlots) & 1) ^ 1, abort_flag)) break;
+      const bool whole = j0 == 0 && n == sp.nt;
+      if (lane == 0) {
+        volatile int* p = segs + slot * L::kSegInts;
+        p[0] = b; p[1] = h; p[2] = rg; p[3] = j0;
+        p[4] = n; p[5] = Lb; p[6] = nb; p[7] = (k == 0 ? 1 : 0) | (whole ? 2 : 0);
+        mbar_arrive(&bars[L::SEG_FULL + slot]);
+      }
+      if (n == 0) break;
+      if (k == 0 && j0 > 0) meta_mid = 1;
+      if (j0 == 0 && n < sp.nt) {   // this CTA starts a unit that others finish
+        const long long x = p0 + Split::tile_at(sp.nt - 1, w);
+        long long c = x * a.grid / T;
+        while (c + 1 < a.grid && T * (c + 1) / a.grid <= x) ++c;
+        while (c > 0 && T * c / a.grid > x) --c;
+        meta_c1 = (int)c;
+        meta_slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
+        meta_b = b; meta_h = h; meta_rg = rg;
+      }
+      ++k;
+
+      const int np = (Lb + kTile - 1) / kTile;
+      const int rows = a.G * nb - rg * 2 * kTile;
+      const bool pair = rows > kTile;
+      const int bh = b * t.Hkv + h;
+      const int npg = kPaged ? kTile / t.page_size : 0;
+      const int32_t* table = kPaged ? t.block_table + (size_t)b * t.max_pages : nullptr;
+      // cache row of this lane's page of tile j (the row past the cache,
+      // which the TMA fills with zeros, for pages past the cached keys)
+      auto page_row = [&](int j) -> int {
+        const int pg = j * npg + lane;
+        return (lane < npg && j < np && pg * t.page_size < Lb)
+                   ? paged_cache_row(table[pg], t.num_pages, t.Hkv, h, t.page_size, a.oob_row)
+                   : a.oob_row;
+      };
+      // one K or V tile into ring position pos
+      auto load = [&](int pos, int j, int row, bool is_v) -> bool {
+        const int st = pos % NS;
+        bool w_ok = true;
+        if (lane == 0) {
+          w_ok = mbar_wait(&bars[L::EMPTY + st], ((pos / NS) & 1) ^ 1, abort_flag);
+          if (w_ok) mbar_arrive_expect_tx(&bars[L::FULL + st], L::kTileBytes);
+        }
+        if (!__shfl_sync(0xffffffffu, w_ok, 0)) return false;
+        ++armed;
+        uint8_t* dst = smem + L::kKV + st * L::kTileBytes;
+        if (j >= np) {
+          if (lane < D / 64)
+            tma_load_3d(dst + lane * L::kBox, is_v ? &tvn : &tkn, lane * 64, (j - np) * kTile, bh,
+                        &bars[L::FULL + st]);
+        } else if constexpr (kPaged) {
+          if (lane < npg) {
+            if constexpr (D == 128)
+              tma_load_4d(dst + lane * t.page_size * 256, is_v ? &tv : &tk, row >> 3,
+                          &bars[L::FULL + st]);
+            else
+              tma_load_2d(dst + lane * t.page_size * 128, is_v ? &tv : &tk, 0, row,
+                          &bars[L::FULL + st]);
+          }
+        } else {
+          if (lane < D / 64)
+            tma_load_3d(dst + lane * L::kBox, is_v ? &tv : &tk, lane * 64, j * kTile, bh,
+                        &bars[L::FULL + st]);
+        }
+        return true;
+      };
+      int r_cur = kPaged ? page_row(j0) : 0, r_next = r_cur;
+      if (pair) {
+        for (int j = 0; ok && j < n; ++j) {
+          r_next = kPaged && j + 1 < n ? page_row(j0 + j + 1) : 0;
+          ok = load(g + 2 * j, j0 + j, r_cur, false) && load(g + 2 * j + 1, j0 + j, r_cur, true);
+          r_cur = r_next;
+        }
+      } else {
+        ok = load(g, j0, r_cur, false);
+        r_next = kPaged && n > 1 ? page_row(j0 + 1) : 0;
+        for (int j = 0; ok && j < n; ++j) {
+          const int r2 = kPaged && j + 2 < n ? page_row(j0 + j + 2) : 0;
+          if (j + 1 < n) ok = load(k_pos(g, j + 1, false), j0 + j + 1, r_next, false);
+          if (ok) ok = load(v_pos(g, j, n, false), j0 + j, r_cur, true);
+          r_cur = r_next;
+          r_next = r2;
+        }
+      }
+      g += 2 * n;
+      j0 += n - 1;   // (only its being the unit's last tile matters below)
+      if (j0 == sp.nt - 1) next_unit(); else more = false;
+    }
+    if (lane == 0) {
+      int* m = a.meta + 8 * blockIdx.x;
+      m[0] = meta_mid; m[1] = meta_c1; m[2] = meta_slot;
+      m[3] = meta_b; m[4] = meta_h; m[5] = meta_rg;
+      // every issued load must land before the CTA may exit
+      for (int j = armed - NS > 0 ? armed - NS : 0; j < armed; ++j)
+        mbar_wait(&bars[L::FULL + j % NS], (j / NS) & 1, nullptr);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t q_base = smem_u32(smem + L::kQ), kv_base = smem_u32(smem + L::kKV);
+    auto commit = [&](int bar) {
+      if (elect_one()) tc::commit(&bars[bar]);
+      __syncwarp();
+    };
+    int k = 0, g = 0, qt = 0, pw0 = 0, pw1 = 0;
+    bool ok = true;
+    Seg s;
+    while (ok && next_seg(k, s)) {
+      const bool pair = group_rows(s) > kTile;
+      const int n = s.n, ns = pair ? 2 * n : n, np = s.np();
+      // strides of a tile: a page of d = 128 lands as 8-row groups of [half 0
+      // | half 1], everything else as 64-column halves
+      auto grouped = [&](int j) { return kPaged && D == 128 && s.j0 + j < np; };
+      auto do_s = [&](int st) -> bool {
+        const int sl = st & 1, j = pair ? st >> 1 : st;
+        const int pos = k_pos(g, j, pair), q = pair ? qt + sl : qt;
+        if (pair ? st < 2 : st == 0) {
+          if (!mbar_wait_warp(&bars[L::Q_FULL + (q & 1)], (q >> 1) & 1, abort_flag)) return false;
+        }
+        if (!pair || sl == 0) {
+          if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) return false;
+        }
+        tc::fence_after();
+        const uint32_t half = grouped(j) ? 1024u : (uint32_t)L::kBox;
+        const uint64_t dq = tc::smem_desc_sw128(q_base + (q & 1) * L::kTileBytes, 16, 1024);
+        const uint64_t dk = tc::smem_desc_sw128(kv_base + (pos % NS) * L::kTileBytes, 16,
+                                                grouped(j) ? 2048 : 1024);
+        if (elect_one()) {
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.o[row * D + lane * E + e] = __float2bfloat16_rn(l > 0.f ? o[e] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ss(tmem + 128u * sl, dq + (uint64_t)(((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4),
+                       dk + (uint64_t)(((kk >> 2) * half + (kk & 3) * 32) >> 4), kIdescS,
+                       kk > 0 ? 1u : 0u);
+        }
+        __syncwarp();
+        commit(L::S_FULL + sl);
+        if (!pair || sl == 1) commit(L::EMPTY + pos % NS);
+        if (pair ? st >= ns - 2 : st == ns - 1) commit(L::Q_EMPTY + (q & 1));
+        return true;
+      };
+      for (int st = 0; ok && st < 2 && st < ns; ++st) ok = do_s(st);
+      for (int st = 0; ok && st < ns; ++st) {
+        const int sl = st & 1, j = pair ? st >> 1 : st;
+        const int pos = v_pos(g, j, n, pair);
+        int& pw = sl ? pw1 : pw0;
+        if (!mbar_wait_warp(&bars[L::P_FULL + sl], pw & 1, abort_flag)) { ok = false; break; }
+        ++pw;
+        if (!pair || sl == 0) {
+          if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) { ok = false; break; }
+        }
+        tc::fence_after();
+        const uint32_t half = grouped(j) ? 1024u : (uint32_t)L::kBox;
+        const uint32_t grp = grouped(j) ? 2048u : 1024u;
+        const uint64_t dv = tc::smem_desc_sw128(kv_base + (pos % NS) * L::kTileBytes, half, grp);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc::mma_ts(tmem + 256u + (uint32_t)D * sl, tmem + 128u * sl + kk * 8,
+                       dv + (uint64_t)((kk * 2 * grp) >> 4), kIdescPV, (st >= 2 || kk > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        if (!pair || sl == 1) commit(L::EMPTY + pos % NS);
+        if (st >= ns - 2) commit(L::O_FULL + sl);
+        if (st + 2 < ns) ok = do_s(st + 2);
+      }
+      g += 2 * n;
+      qt += pair ? 2 : 1;
+    }
+    // every MMA of this CTA must be complete before TMEM is released
+    commit(L::MMA_DONE);
+    mbar_wait_warp(&bars[L::MMA_DONE], 0, nullptr);
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ Q rows
+    // Row r of the unit is node r % nb of head r / nb.  A lane copies chunk
+    // `c` of every (32 / chunks)-th row; the warps take 64 rows of a tile each.
+    constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+    const int c = lane % kChunks;
+    int k = 0, qt = 0;
+    bool ok = true;
+    Seg s;
+    while (ok && next_seg(k, s)) {
+      const int rows = group_rows(s);
+      const int nq = rows > kTile ? 2 : 1;
+      const int dg = kStep / s.nb, di = kStep % s.nb;
+      const __nv_bfloat16* qb =
+          t.q + ((size_t)s.b * t.Hq + (size_t)s.h * a.G) * t.Nq * D + c * 8;
+      for (int sl = 0; sl < nq; ++sl, ++qt) {
+        if (!mbar_wait_warp(&bars[L::Q_EMPTY + (qt & 1)], ((qt >> 1) & 1) ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = smem_u32(smem + L::kQ + (qt & 1) * L::kTileBytes) +
+                             (uint32_t)(c >> 3) * L::kBox;
+        int r = (warp - 10) * 64 + lane / kChunks;
+        const int r_end = (warp - 10) * 64 + 64, r0 = s.rg * 2 * kTile + sl * kTile;
+        int gh = (r0 + r) / s.nb, i = (r0 + r) % s.nb;
+        for (; r < r_end && sl * kTile + r < rows; r += kStep) {
+          cp_async_16(dst + sw128_offset(r, c & 7), qb + ((size_t)gh * t.Nq + i) * D);
+          gh += dg;
+          i += di;
+          if (i >= s.nb) { i -= s.nb; ++gh; }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::Q_FULL + (qt & 1)]);
+      }
+    }
+    // rows of the nodes a sequence does not have
+    if (t.new_lens) {
+      for (long long x = blockIdx.x * 2 + (warp - 10); x < (long long)t.B * t.Hq; x += a.grid * 2) {
+        const int nb = live_nodes(t, (int)(x / t.Hq));
+        uint4* o = reinterpret_cast<uint4*>(t.o + (x * t.Nq + nb) * D);
+        for (int e = lane; e < (t.Nq - nb) * (D / 8); e += 32) o[e] = make_uint4(0, 0, 0, 0);
+        if (t.lse)
+          for (int e = nb + lane; e < t.Nq; e += 32) t.lse[x * t.Nq + e] = -INFINITY;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int sl = warp >> 2;                 // slot
+    const int r = (warp & 3) * 32 + lane;     // row of the slot = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t scol = tmem + lane_off + 128u * sl;
+    const uint32_t ocol = tmem + lane_off + 256u + (uint32_t)D * sl;
+    const float sl2 = t.scale_log2;
+    const bool o_32B = (reinterpret_cast<uintptr_t>(t.o) & 31) == 0;
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
+    int k = 0, g = 0, sw = 0, ow0 = 0, ow1 = 0;
+    bool ok = true;
+    Seg s;
+    // a failed read of the ring is voted on below like any other failure
+    bool live = next_seg(k, s);
+    while (!bar_vote_or(1, 256, !live)) {
+      const int rows = group_rows(s), n = s.n, np = s.np();
+      const bool pair = rows > kTile;
+      const int lr = pair ? sl * kTile + r : r;          // row within the group
+      const int warp_row = lr - lane;
+      const bool idle = warp_row >= rows;                // no live row in this warp
+      const int rr = s.rg * 2 * kTile + (lr < rows ? lr : rows - 1);
+      const int head = rr / s.nb, node = rr - head * s.nb;
+      float m_run = -INFINITY, l_run = 0.f;
+      const int steps = pair ? n : (n + 1 - sl) / 2;
+      for (int x = 0; x < steps; ++x) {
+        const int j = pair ? x : 2 * x + sl;
+        const int jt = s.j0 + j;                         // tile of the unit
+        // keys of the tile that exist; the rest are masked, and their values
+        // cleared, as anything may be stored there
+        const int valid = jt < np ? s.L - jt * kTile : s.nb - (jt - np) * kTile;
+        uint32_t bits[4] = {0u, 0u, 0u, 0u};
+        const bool masked = jt >= np || valid < kTile;
+        if (masked && !idle) {
+          if (jt < np) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int e = valid - 32 * c;
+              bits[c] = e >= 32 ? 0xffffffffu : (e <= 0 ? 0u : (1u << e) - 1u);
+            }
+          } else {
+            // the node and its ancestors among drafts [base, base + 128)
+            const int base = (jt - np) * kTile;
+            const int32_t* par = t.parents + (size_t)s.b * t.Nq;
+            int v = node;
+            while (v >= base) {
+              const int e = v - base;
+              if (e < kTile) {
+                const uint32_t bit = 1u << (e & 31);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) bits[c] |= (e >> 5) == c ? bit : 0u;
+              }
+              const int p = par[v];
+              if (p < -1 || p >= v) {
+                atomicExch(&g_device_status, (int)ATTN_ERANGE);
+                break;
+              }
+              v = p;
+            }
+          }
+        }
+        if (!mbar_wait_warp(&bars[L::S_FULL + sl], sw & 1, abort_flag)) { ok = false; break; }
+        ++sw;
+        tc::fence_after();
+        if (valid < kTile && (!pair || sl == 0)) {
+          // (a pair's second product on this tile is issued after the first,
+          // which waits for this slot's P)
+          const int pos = v_pos(g, j, n, pair);
+          if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) { ok = false; break; }
+          if (r >= valid) {
+            const bool grouped = kPaged && D == 128 && jt < np;
+            uint8_t* vt = smem + L::kKV + (pos % NS) * L::kTileBytes +
+                          (grouped ? (r >> 3) * 2048 + (r & 7) * 128 : r * 128);
+#pragma unroll
+            for (int hb = 0; hb < D / 64; ++hb)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(vt + hb * (grouped ? 1024 : L::kBox) + c * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (idle) {
+          tc::fence_before();
+          mbar_arrive(&bars[L::P_FULL + sl]);
+          continue;
+        }
+        // An unmasked tile after the row's first: the running max usually
+        // stands (O is rescaled only when a score passes it by more than 8
+        // in log2 units), so P is computed with it from a single read of S
+        // and kept if no row of the warp needs a rescale.
+        if (!masked && m_run != -INFINITY) {
+          const float2 c_sl2 = make_float2(sl2, sl2), c_m = make_float2(-m_run, -m_run);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t pk[64];
+          float rsum = 0.f;
+#pragma unroll
+          for (int c8 = 0; c8 < 2; ++c8) {
+            float sv[64];
+            tc::ld32f(scol + 64 * c8, sv);
+            tc::ld32f(scol + 64 * c8 + 32, sv + 32);
+            tc::wait_ld();
+            float2 rs2 = make_float2(0.f, 0.f), rs3 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              m4[e & 3] = max3(m4[e & 3], sv[2 * e], sv[2 * e + 1]);
+              const float2 y = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), c_sl2, c_m);
+              const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              if (e & 1) rs3 = __fadd2_rn(rs3, p); else rs2 = __fadd2_rn(rs2, p);
+              pk[32 * c8 + e] = pack_bf16x2(p.x, p.y);
+            }
+            rs2 = __fadd2_rn(rs2, rs3);
+            rsum += rs2.x + rs2.y;
+          }
+          const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+          if (__all_sync(0xffffffffu, !(m_tile > m_run + kRescaleLog2))) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::st16(scol + 16 * c, pk + 16 * c);
+            l_run += rsum;
+            tc::wait_st();
+            tc::fence_before();
+            mbar_arrive(&bars[L::P_FULL + sl]);
+            continue;
+          }
+        }
+        // two passes over S, in chunks of 32 keys: a chunk that no row of the
+        // warp sees is skipped, one that every row sees takes no mask
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t w = !masked ? 0xffffffffu
+                                     : (c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3]);
+          if (!__any_sync(0xffffffffu, w != 0u)) continue;
+          float sv[32];
+          tc::ld32f(scol + 32 * c, sv);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (w >> e) & 1u ? sv[e] : -INFINITY);
+        }
+        const float m_tile = mx * sl2;
+        const bool need = m_tile > m_run + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = need ? m_tile : m_run;
+          if (x > 0) {
+            const float f = (need && m_run != -INFINITY) ? exp2_approx(m_run - m_new) : 1.f;
+            l_run *= f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tc::ld32f(ocol + 32 * c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tc::st32f(ocol + 32 * c, o);
+            }
+          }
+          m_run = m_new;
+        }
+        const float m_use = m_run == -INFINITY ? 0.f : m_run;
+        float rs = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t w = !masked ? 0xffffffffu
+                                     : (c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3]);
+          uint32_t pk[16];
+          if (!__any_sync(0xffffffffu, w != 0u)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          } else {
+            float sv[32];
+            tc::ld32f(scol + 32 * c, sv);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x0 = (w >> (2 * e)) & 1u ? sv[2 * e] : -INFINITY;
+              const float x1 = (w >> (2 * e + 1)) & 1u ? sv[2 * e + 1] : -INFINITY;
+              const float p0 = exp2_approx(fmaf(x0, sl2, -m_use));
+              const float p1 = exp2_approx(fmaf(x1, sl2, -m_use));
+              rs += p0 + p1;
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+          }
+          tc::st16(scol + 16 * c, pk);
+        }
+        l_run += rs;
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&bars[L::P_FULL + sl]);
+      }
+      // ---- segment end
+      if (!pair) ml[sl * kTile + r] = make_float2(m_run, l_run);
+      // (also orders the exchange; every softmax thread leaves on the same vote)
+      if (bar_vote_or(2, 256, !ok)) break;
+      float f0 = 0.f, f1 = 0.f, m = m_run, l = l_run;
+      const bool two = !pair && n > 1;                   // slot 1 took part as well
+      if (!pair) {
+        const float2 x0 = ml[r], x1 = ml[kTile + r];
+        m = fmaxf(x0.x, x1.x);
+        const float w0 = x0.x == -INFINITY ? 0.f : exp2_approx(x0.x - m);
+        const float w1 = x1.x == -INFINITY ? 0.f : exp2_approx(x1.x - m);
+        l = x0.y * w0 + x1.y * w1;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        f0 = w0 * inv;
+        f1 = w1 * inv;
+      } else {
+        f0 = l > 0.f ? 1.f / l : 0.f;
+      }
+      if (!pair || sl == 0) {
+        if (!mbar_wait_warp(&bars[L::O_FULL], ow0 & 1, abort_flag)) ok = false;
+      }
+      if (two || (pair && sl == 1)) {
+        if (!mbar_wait_warp(&bars[L::O_FULL + 1], ow1 & 1, abort_flag)) ok = false;
+      }
+      ++ow0;
+      if (two || pair) ++ow1;
+      tc::fence_after();
+      const bool direct = (s.flags & 2) != 0;
+      const int slot = 2 * blockIdx.x + ((s.flags & 1) ? 0 : 1);
+      const bool store = !idle && lr < rows;
+      const size_t orow =
+          ((size_t)s.b * t.Hq + (size_t)s.h * a.G + head) * t.Nq + node;
+      const size_t prow = (size_t)slot * a.RP + lr;
+      // pair: all columns of the own slot; else half of the columns of both
+      const uint32_t oa = tmem + lane_off + 256u + (pair ? (uint32_t)D * sl : 0u);
+      const int c_lo = pair ? 0 : sl * (D / 64), c_hi = pair ? D / 32 : (sl + 1) * (D / 64);
+      if (!idle) {
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; ++c) {
+          float o[32];
+          tc::ld32f(oa + 32 * c, o);
+          if (two) {
+            float o1[32];
+            tc::ld32f(oa + D + 32 * c, o1);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+          } else {
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f0;
+          }
+          if (store && direct) {
+            __nv_bfloat16* dst = t.o + orow * D + 32 * c;
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[q].x = pack_bf16x2(o[8 * q + 0], o[8 * q + 1]);
+              v[q].y = pack_bf16x2(o[8 * q + 2], o[8 * q + 3]);
+              v[q].z = pack_bf16x2(o[8 * q + 4], o[8 * q + 5]);
+              v[q].w = pack_bf16x2(o[8 * q + 6], o[8 * q + 7]);
+            }
+            if (o_32B) {
+              st_global_32B(dst, v[0], v[1]);
+              st_global_32B(dst + 16, v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + 8 * q) = v[q];
+            }
+          } else if (store) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+      }
+      if (store && (pair || sl == 0)) {
+        const float lse = l > 0.f ? m + __log2f(l) : -INFINITY;
+        if (!direct) a.part_lse[prow] = lse;
+        else if (t.lse) t.lse[orow] = l > 0.f ? lse * kLn2 : -INFINITY;
+      }
+      tc::fence_before();
+      g += 2 * n;
+      // both slots' O have been read before either slot's next P is released
+      // (the vote at the loop's head)
+      live = ok && next_seg(k, s);
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
 }
+
+// Joins the partial results of the units that cross a cut: blockIdx.x = the CTA
+// in which the unit starts, blockIdx.y = a chunk of its rows.  The parts' log-
+// sum-exps of the chunk's rows go to shared memory; a thread then merges four
+// columns of one row over the parts, in order.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(tr::Args a) {
+  using namespace tr;
+  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int HB = kJoinThreads * 4 / D;    // rows of a chunk
+  extern __shared__ float js[];               // float [parts][HB], then int [parts]
+  __shared__ int s_np;
+  int* slots = reinterpret_cast<int*>(js + (size_t)a.grid * HB);
+  const TreeArgs& t = a.t;
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* m = a.meta + 8 * c0;
+  const int c1 = m[1];
+  if (c1 < 0) return;
+  const int b = m[3], h = m[4], rg = m[5];
+  const int nb = live_nodes(t, b);
+  int rows = a.G * nb - rg * 2 * kTile;
+  if (rows > 2 * kTile) rows = 2 * kTile;
+  const int r0 = blockIdx.y * HB;
+  if (r0 >= rows) return;
+  if (threadIdx.x < 32) {
+    // the starting CTA's part, then those of the CTAs whose first segment
+    // continues the unit (a CTA without a tile has none)
+    int cnt = 1;
+    if (lane == 0) slots[0] = m[2];
+    for (int base = c0 + 1; base <= c1; base += 32) {
+      const int c = base + lane;
+      const bool has = c <= c1 && a.meta[8 * c] != 0;
+      const unsigned bal = __ballot_sync(0xffffffffu, has);
+      if (has) slots[cnt + __popc(bal & ((1u << lane) - 1))] = 2 * c;
+      cnt += __popc(bal);
+    }
+    if (lane == 0) s_np = cnt;
+  }
+  __syncthreads();
+  const int np = s_np;
+  for (int x = threadIdx.x; x < np * HB; x += kJoinThreads) {
+    const int p = x / HB, r = r0 + x % HB;
+    js[x] = r < rows ? a.part_lse[(size_t)slots[p] * a.RP + r] : -INFINITY;
+  }
+  __syncthreads();
+  const int lr = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
+  const int r = r0 + lr;
+  if (r >= rows) return;
+  float mx = -INFINITY, sum = 0.f;
+  for (int p = 0; p < np; ++p) mx = fmaxf(mx, js[p * HB + lr]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < np; ++p) {
+    const float w = mx == -INFINITY ? 0.f : exp2_approx(js[p * HB + lr] - mx);
+    const float4 v =
+        *reinterpret_cast<const float4*>(a.part_o + ((size_t)slots[p] * a.RP + r) * D + col);
+    sum += w;
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int rr = rg * 2 * kTile + r;
+  const int head = rr / nb;
+  const size_t row = ((size_t)b * t.Hq + (size_t)h * a.G + head) * t.Nq + (rr - head * nb);
+  uint2 o;
+  o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(t.o + row * D + col) = o;
+  if (t.lse && col == 0) t.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host side
 
 bool tree_supported(int B, int Nq, int d) {
-  return (d == 64 || d == 128) && Nq <= 1024 && B <= 2048;
+  return (d == 64 || d == 128) && Nq <= 1024 && B <= tr::kMaxB;
 }
+
+namespace {
+int rows_per_slot(int Hq, int Hkv, int Nq) {
+  const long long rows = (long long)(Hq / Hkv) * Nq;
+  return rows < 2 * tr::kTile ? (int)rows : 2 * tr::kTile;
+}
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <int D, bool kPaged>
+int launch_tree_t(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                  const CUtensorMap& tkn, const CUtensorMap& tvn, cudaStream_t st) {
+  auto kern = tree_tc_kernel<D, kPaged>;
+  constexpr int smem = tr::Smem<D>::kTotal;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return ATTN_ECUDA;
+  const int rc = launch_programmatic(kern, dim3(a.grid), dim3(tr::kThreads), smem, st, tk, tv, tkn,
+                                     tvn, a);
+  if (rc != ATTN_OK) return rc;
+  constexpr int HB = kJoinThreads * 4 / D;
+  return launch_programmatic(tree_join_kernel<D>, dim3(a.grid, (a.RP + HB - 1) / HB),
+                             dim3(kJoinThreads), (size_t)a.grid * (HB + 1) * 4, st, a);
+}
+}  // namespace
 
 size_t tree_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int num_sms) {
-  (void)B; (void)Hq; (void)Hkv; (void)Nq; (void)d; (void)num_sms;
-  return 256;
+  (void)B;
+  const size_t rp = (size_t)rows_per_slot(Hq, Hkv, Nq), slots = 2 * (size_t)num_sms;
+  return round256(slots * rp * d * sizeof(float)) + round256(slots * rp * sizeof(float)) +
+         round256((size_t)num_sms * 8 * sizeof(int));
 }
 
-int launch_tree(const TreeArgs& a, int d, void* workspace, int num_sms, cudaStream_t st) {
-  (void)workspace; (void)num_sms;
-  const long long rows = (long long)a.B * a.Hq * a.Nq;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  if (d == 128) tree_rows_kernel<128><<<grid, 128, 0, st>>>(a);
-  else tree_rows_kernel<64><<<grid, 128, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ECUDA;
+int launch_tree(const TreeArgs& t, int d, void* workspace, int num_sms, cudaStream_t st) {
+  tr::Args a;
+  a.t = t;
+  a.G = t.Hq / t.Hkv;
+  a.RP = rows_per_slot(t.Hq, t.Hkv, t.Nq);
+  a.grid = num_sms;
+  const size_t slots = 2 * (size_t)num_sms;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.part_o = reinterpret_cast<float*>(w);
+  w += round256(slots * a.RP * d * sizeof(float));
+  a.part_lse = reinterpret_cast<float*>(w);
+  w += round256(slots * a.RP * sizeof(float));
+  a.meta = reinterpret_cast<int*>(w);
+  // the drafts [B * Hkv, Nq, d] and a contiguous cache [B * Hkv, Nk, d] in
+  // boxes of 128 rows x 64 columns; a paged cache page by page
+  CUtensorMap tk, tv, tkn, tvn;
+  const uint64_t mats = (uint64_t)t.B * t.Hkv;
+  if (make_tmap_3d_bf16(&tkn, t.kn, d, t.Nq, mats, 64, tr::kTile) != ATTN_OK) return ATTN_ECUDA;
+  if (make_tmap_3d_bf16(&tvn, t.vn, d, t.Nq, mats, 64, tr::kTile) != ATTN_OK) return ATTN_ECUDA;
+  a.oob_row = 0;
+  if (!t.block_table) {
+    if (make_tmap_3d_bf16(&tk, t.kc, d, t.Nk, mats, 64, tr::kTile) != ATTN_OK) return ATTN_ECUDA;
+    if (make_tmap_3d_bf16(&tv, t.vc, d, t.Nk, mats, 64, tr::kTile) != ATTN_OK) return ATTN_ECUDA;
+    return d == 128 ? launch_tree_t<128, false>(a, tk, tv, tkn, tvn, st)
+                    : launch_tree_t<64, false>(a, tk, tv, tkn, tvn, st);
+  }
+  const uint64_t rows = (uint64_t)t.num_pages * t.Hkv * t.page_size;
+  a.oob_row = (int)rows;
+  if (d == 128) {
+    const uint32_t groups = (uint32_t)t.page_size / 8;
+    if (make_tmap_grouped_bf16(&tk, t.kc, rows, groups) != ATTN_OK) return ATTN_ECUDA;
+    if (make_tmap_grouped_bf16(&tv, t.vc, rows, groups) != ATTN_OK) return ATTN_ECUDA;
+    return launch_tree_t<128, true>(a, tk, tv, tkn, tvn, st);
+  }
+  const uint32_t ps = (uint32_t)t.page_size;
+  if (make_tmap_2d_bf16(&tk, t.kc, d, rows, 64, ps) != ATTN_OK) return ATTN_ECUDA;
+  if (make_tmap_2d_bf16(&tv, t.vc, d, rows, 64, ps) != ATTN_OK) return ATTN_ECUDA;
+  return launch_tree_t<64, true>(a, tk, tv, tkn, tvn, st);
 }
 
 }  // namespace attn
