@@ -559,6 +559,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       const int lr = pair ? sl * kTile + r : r;          // row within the group
       const int warp_row = lr - lane;
       const bool idle = warp_row >= rows;                // no live row in this warp
+      const bool dead = lr >= rows;                      // computes on anything, is not stored
       const int rr = s.rg * 2 * kTile + (lr < rows ? lr : rows - 1);
       const int head = rr / s.nb, node = rr - head * s.nb;
       float m_run = -INFINITY, l_run = 0.f;
@@ -625,11 +626,12 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
           mbar_arrive(&bars[L::P_FULL + sl]);
           continue;
         }
-        // An unmasked tile after the row's first: the running max usually
+        // An unmasked tile after the slot's first: the running max usually
         // stands (O is rescaled only when a score passes it by more than 8
         // in log2 units), so P is computed with it from a single read of S
-        // and kept if no row of the warp needs a rescale.
-        if (!masked && m_run != -INFINITY) {
+        // and kept if no live row of the warp needs a rescale.  (The branch
+        // is on what the whole warp shares: tcgen05 moves are warp-wide.)
+        if (!masked && x > 0) {
           const float2 c_sl2 = make_float2(sl2, sl2), c_m = make_float2(-m_run, -m_run);
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           uint32_t pk[64];
@@ -653,7 +655,8 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
             rsum += rs2.x + rs2.y;
           }
           const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
-          if (__all_sync(0xffffffffu, !(m_tile > m_run + kRescaleLog2))) {
+          const bool keep = m_run != -INFINITY && !(m_tile > m_run + kRescaleLog2);
+          if (__all_sync(0xffffffffu, keep || dead)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) tc::st16(scol + 16 * c, pk + 16 * c);
             l_run += rsum;
@@ -678,7 +681,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
           for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (w >> e) & 1u ? sv[e] : -INFINITY);
         }
         const float m_tile = mx * sl2;
-        const bool need = m_tile > m_run + kRescaleLog2;
+        const bool need = !dead && m_tile > m_run + kRescaleLog2;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? m_tile : m_run;
           if (x > 0) {
@@ -739,11 +742,11 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
         const float w0 = x0.x == -INFINITY ? 0.f : exp2_approx(x0.x - m);
         const float w1 = x1.x == -INFINITY ? 0.f : exp2_approx(x1.x - m);
         l = x0.y * w0 + x1.y * w1;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         f0 = w0 * inv;
         f1 = w1 * inv;
       } else {
-        f0 = l > 0.f ? 1.f / l : 0.f;
+        f0 = l == 0.f ? 0.f : 1.f / l;   // (a NaN among the scores stays one)
       }
       if (!pair || sl == 0) {
         if (!mbar_wait_warp(&bars[L::O_FULL], ow0 & 1, abort_flag)) ok = false;
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       tc::fence_after();
       const bool direct = (s.flags & 2) != 0;
       const int slot = 2 * blockIdx.x + ((s.flags & 1) ? 0 : 1);
-      const bool store = !idle && lr < rows;
+      const bool store = !dead;
       const size_t orow =
           ((size_t)s.b * t.Hq + (size_t)s.h * a.G + head) * t.Nq + node;
       const size_t prow = (size_t)slot * a.RP + lr;
@@ -805,9 +808,9 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
         }
       }
       if (store && (pair || sl == 0)) {
-        const float lse = l > 0.f ? m + __log2f(l) : -INFINITY;
+        const float lse = l == 0.f ? -INFINITY : m + __log2f(l);
         if (!direct) a.part_lse[prow] = lse;
-        else if (t.lse) t.lse[orow] = l > 0.f ? lse * kLn2 : -INFINITY;
+        else if (t.lse) t.lse[orow] = lse * kLn2;
       }
       tc::fence_before();
       g += 2 * n;
@@ -880,7 +883,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(tr::Args a) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = 0; p < np; ++p) {
-    const float w = mx == -INFINITY ? 0.f : exp2_approx(js[p * HB + lr] - mx);
+    const float ls = js[p * HB + lr];
+    const float w = ls == -INFINITY ? 0.f : exp2_approx(ls - mx);
     const float4 v =
         *reinterpret_cast<const float4*>(a.part_o + ((size_t)slots[p] * a.RP + r) * D + col);
     sum += w;
@@ -889,7 +893,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(tr::Args a) {
     acc.z = fmaf(w, v.z, acc.z);
     acc.w = fmaf(w, v.w, acc.w);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int rr = rg * 2 * kTile + r;
   const int head = rr / nb;
   const size_t row = ((size_t)b * t.Hq + (size_t)h * a.G + head) * t.Nq + (rr - head * nb);
@@ -897,7 +901,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(tr::Args a) {
   o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(t.o + row * D + col) = o;
-  if (t.lse && col == 0) t.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+  if (t.lse && col == 0) t.lse[row] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host side

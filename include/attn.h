@@ -402,7 +402,8 @@ ATTN_API int kv_append(const void* q, const void* k, const void* v, const int64_
  * block_table == NULL: a contiguous cache [B, Hkv, Nk, d], key_lens NULL =
  * Nk; max_pages, page_size and num_pages are 0.
  *   Cache rows at or beyond key_lens[b], and drafted rows at or beyond
- * new_lens[b], may hold anything, NaN included.
+ * new_lens[b], may hold anything, NaN included; the values of the others are
+ * finite (a masked weight of zero times an infinity is NaN).
  *   Workspace: attn_tree_workspace_size(...) bytes, as for attn_fwd_ws.
  * Errors: ATTN_EINVAL, ATTN_EUNSUPPORTED (d not 64 or 128, Nq > 1024, B >
  * 2048, page_size, sizes of 2^31 rows or more), ATTN_EALIGN,

@@ -123,6 +123,10 @@ CASES = [
     (2, 1, 1, 300, 128, 0, [0, 41], [300, 257]),
     (5, 2, 2, 2, 64, 0, [0, 1, 4000, 64, 2000], [2, 1, 2, 0, 2]),    # split over many CTAs
     (1, 4, 1, 4, 128, 16, [3999], [4]),
+    (4, 8, 8, 3, 128, 16, [4000, 3500, 129, 3900], [3, 2, 3, 1]),    # several tiles of several units a CTA
+    (6, 6, 6, 2, 64, 8, [4000, 3500, 1290, 3900, 2200, 3000], [2, 2, 1, 2, 0, 2]),
+    (4, 24, 6, 33, 128, 32, [2500, 1800, 2100, 40], [33, 32, 9, 33]),   # 132 rows: pairs
+    (5, 20, 4, 26, 64, 0, [2500, 1800, 2100, 40, 1], [26, 25, 9, 26, 1]),
     (40, 4, 4, 2, 64, 32, [i * 17 % 300 for i in range(40)], [i % 3 for i in range(40)]),
 ]
 
@@ -167,6 +171,22 @@ def test_tree_rising_scores(torch, eb):
         x["kc"][int(x["table"][0, j]), :, :m] = x["k"][0][:, 16 * j:16 * j + m]
     o, lse = call(torch, eb, x)
     check(torch, o, lse, want(x))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_nan_stays_in_its_row(torch, eb, d):
+    """A query of NaN among live rows, over enough tiles that every CTA takes
+    several: its row is NaN, the others are what they are without it."""
+    x = make(torch, 4, 16, 8, 7, d, 16, [4000, 3500, 129, 3900], [7, 5, 7, 1], seed=16)
+    w = want(x)
+    x["q"][0, 3, 2] = float("nan")
+    x["q"][3, 15, 0, 1] = float("nan")
+    o, lse = call(torch, eb, x)
+    o, lse = o.cpu(), lse.cpu()
+    for b, h, i in [(0, 3, 2), (3, 15, 0)]:
+        assert bool(torch.isnan(o[b, h, i]).all()) and bool(torch.isnan(lse[b, h, i]))
+        o[b, h, i], lse[b, h, i] = w[0][b, h, i].to(o.dtype), w[1][b, h, i].float()
+    check(torch, o, lse, w)
 
 
 def test_tree_equals_paged_decode_for_a_chain(torch, eb):
