@@ -416,21 +416,71 @@ def rope_apply(x, base=10000.0, pos_offset=0, pairing=0, out=None, stream=None):
     return out
 
 
-def _used_on(stream, *tensors):
-    """Mark tensors allocated here (on the current stream) as used by
-    `stream`, so that the caching allocator keeps their memory until `stream`
-    has passed the call."""
-    torch = _torch()
-    s = _torch_stream(stream)
-    for t in tensors:
-        if t is not None and s != torch.cuda.current_stream(t.device):
-            t.record_stream(s)
+# The serving calls run once per step or per layer, often on small tensors,
+# where the host is what they cost: an argument's type, shape, device and
+# layout are looked at once, and the reason is looked for only when one of
+# them does not fit.
+
+def _check_all(ref, args):
+    """Every (tensor, name, dtype, shape) of `args` has that dtype and shape,
+    is contiguous and on ref's device, a CUDA device, whose index is returned.
+    What is wrong is raised in the library's order: shapes and types of all
+    arguments before devices."""
+    dev = -1
+    try:
+        dev = ref.get_device()
+        for t, _, dtype, shape in args:
+            if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                    and t.is_contiguous()):
+                dev = -1
+                break
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        for t, name, dtype, shape in args:
+            _check_tensor(t, name, dtype)
+            if tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        _check_devices(ref, [(t, name) for t, name, _, _ in args])
+    return dev
 
 
-def _check_shape(t, name, dtype, shape):
-    _check_tensor(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+class _On:
+    """The device and stream of a call.  Makes the device current while the
+    call runs; what is allocated for another stream than the current one is
+    marked as used there, so that the caching allocator keeps its memory until
+    that stream has passed the call."""
+
+    __slots__ = ("guard", "other", "raw")
+
+    def __init__(self, dev, stream):
+        torch = _torch()
+        self.guard = self.other = None
+        if torch.cuda.current_device() != dev:
+            self.guard = torch.cuda.device(dev)
+        self.raw = torch._C._cuda_getCurrentRawStream(dev)
+        if stream is not None and stream.cuda_stream != self.raw:
+            self.other, self.raw = stream, stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def new(self, like, shape, dtype):
+        t = like.new_empty(shape, dtype=dtype)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
 
 
 def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N, index=None,
@@ -445,47 +495,44 @@ def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N,
     there is none; state_out int32 [2], the queue's new state (a tensor of its
     own: pass it as the next call's state).  Page shortage is reported by
     device_status() (ATTN_ERANGE)."""
-    torch = _torch()
-    _check_tensor(block_table, "block_table", torch.int32, 2)
+    i32 = _torch().int32
+    _check_tensor(block_table, "block_table", i32, 2)
+    _check_tensor(free_pages, "free_pages", i32, 1)
     B, max_pages = block_table.shape
-    _check_shape(old_lens, "old_lens", torch.int32, (B,))
-    _check_shape(new_lens, "new_lens", torch.int32, (B,))
-    _check_tensor(free_pages, "free_pages", torch.int32, 1)
-    _check_shape(state, "state", torch.int32, (2,))
+    num_pages = free_pages.numel()
+    args = [(old_lens, "old_lens", i32, (B,)), (new_lens, "new_lens", i32, (B,)),
+            (free_pages, "free_pages", i32, (num_pages,)), (state, "state", i32, (2,))]
     if index is not None:
-        _check_shape(index, "index", torch.int32, (B, N))
+        args.append((index, "index", i32, (B, N)))
     if slots is not None:
-        _check_shape(slots, "slots", torch.int32, (B, N))
+        args.append((slots, "slots", i32, (B, N)))
     if state_out is not None:
-        _check_shape(state_out, "state_out", torch.int32, (2,))
-    _check_devices(block_table, [(old_lens, "old_lens"), (new_lens, "new_lens"),
-                                 (free_pages, "free_pages"), (state, "state"), (index, "index"),
-                                 (slots, "slots"), (state_out, "state_out")])
-    with torch.cuda.device(block_table.device):
+        args.append((state_out, "state_out", i32, (2,)))
+    with _On(_check_all(block_table, args), stream) as on:
         if slots is None:
-            slots = torch.empty((B, N), dtype=torch.int32, device=block_table.device)
-            _used_on(stream, slots)
+            slots = on.new(block_table, (B, N), i32)
         if state_out is None:
-            state_out = torch.empty_like(state)
-            _used_on(stream, state_out)
-        rc = lib().paged_plan(_ptr(old_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_pages),
-                              _ptr(state), _ptr(state_out), _ptr(index), _ptr(slots), B, N,
-                              max_pages, int(page_size), free_pages.numel(), _stream(stream))
-    _raise(rc, "paged_plan")
+            state_out = on.new(block_table, (2,), i32)
+        rc = lib().paged_plan(old_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                              free_pages.data_ptr(), state.data_ptr(), state_out.data_ptr(),
+                              _data(index), slots.data_ptr(), B, N, max_pages, int(page_size),
+                              num_pages, on.raw)
+    if rc != 0:
+        raise AttnError(rc, "paged_plan")
     return slots, state_out
 
 
 def _check_rows(t, name, shape):
-    """A bf16 [B, H, N, d] argument that may be a strided view with d
-    contiguous."""
+    """A bf16 [B, H, N, d] argument (of this shape, if one is given) that may
+    be a strided view with d contiguous."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 4:
         raise ValueError(f"{name} must have 4 dimensions")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.stride(3) != 1 and t.shape[3] > 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
@@ -507,58 +554,69 @@ def kv_append(k, v=None, slots=None, k_cache=None, v_cache=None, q=None, positio
     is made when return_k is set (by default: when nothing is stored) or k_out
     is given.  q_out / k_out may be q / k themselves."""
     torch = _torch()
+    bf, i32 = torch.bfloat16, torch.int32
     _check_rows(k, "k", None)
-    B, Hkv, N, d = k.shape
+    B, Hkv, N, d = shape = k.shape
     Hq = 0
+    rows = [(k, "k")]
+    args = []
     if q is not None:
         _check_rows(q, "q", None)
-        if (q.shape[0], q.shape[2], q.shape[3]) != (B, N, d):
-            raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)}")
-        Hq = q.shape[1]
+        Bq, Hq, Nq, dq = q.shape
+        if Bq != B or Nq != N or dq != d:
+            raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(shape)}")
         if positions is None:
             raise ValueError("kv_append rotates q: it needs positions")
+        rows.append((q, "q"))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if len({x is None for x in (v, slots, k_cache, v_cache)}) != 1:
-        raise ValueError("v, slots, k_cache and v_cache go together")
     num_pages = page_size = 0
     if slots is not None:
-        _check_rows(v, "v", k.shape)
-        _check_shape(slots, "slots", torch.int32, (B, N))
-        _check_tensor(k_cache, "k_cache", torch.bfloat16, 4)
-        _check_shape(v_cache, "v_cache", torch.bfloat16, k_cache.shape)
-        num_pages, hc, page_size, dc = k_cache.shape
-        if (hc, dc) != (Hkv, d):
-            raise ValueError(f"cache {tuple(k_cache.shape)} does not match k{tuple(k.shape)}")
+        if v is None or k_cache is None or v_cache is None:
+            raise ValueError("v, slots, k_cache and v_cache go together")
+        _check_rows(v, "v", shape)
+        rows.append((v, "v"))
+        _check_tensor(k_cache, "k_cache", bf, 4)
+        num_pages, hc, page_size, dc = cs = k_cache.shape
+        if hc != Hkv or dc != d:
+            raise ValueError(f"cache {tuple(cs)} does not match k{tuple(shape)}")
+        args += [(slots, "slots", i32, (B, N)), (k_cache, "k_cache", bf, cs),
+                 (v_cache, "v_cache", bf, cs)]
+    elif v is not None or k_cache is not None or v_cache is not None:
+        raise ValueError("v, slots, k_cache and v_cache go together")
     if positions is not None:
-        _check_shape(positions, "positions", torch.int32, (B, N))
+        args.append((positions, "positions", i32, (B, N)))
     if return_k is None:
         return_k = slots is None
-    if k_out is not None or return_k:
-        if positions is None:
-            raise ValueError("kv_append returns rotated keys: it needs positions")
+    if (return_k or k_out is not None) and positions is None:
+        raise ValueError("kv_append returns rotated keys: it needs positions")
     if q_out is not None:
-        _check_shape(q_out, "q_out", torch.bfloat16, q.shape)
+        args.append((q_out, "q_out", bf, q.shape))
     if k_out is not None:
-        _check_shape(k_out, "k_out", torch.bfloat16, k.shape)
-    _check_devices(k, [(q, "q"), (v, "v"), (slots, "slots"), (k_cache, "k_cache"),
-                       (v_cache, "v_cache"), (positions, "positions"), (q_out, "q_out"),
-                       (k_out, "k_out")])
-    strides = (ctypes.c_int64 * 9)(*[t.stride(j) if t is not None else 0
-                                     for t in (q, k, v) for j in range(3)])
-    with torch.cuda.device(k.device):
+        args.append((k_out, "k_out", bf, shape))
+    dev = _check_all(k, args)
+    for t, n in rows:
+        if t.get_device() != dev:
+            _check_devices(k, [(t, n)])
+    kb, kh, kt, _ = k.stride()
+    qb, qh, qt, _ = (0, 0, 0, 0) if q is None else q.stride()
+    vb, vh, vt, _ = (0, 0, 0, 0) if v is None else v.stride()
+    with _On(dev, stream) as on:
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _used_on(stream, q_out)
+            q_out = on.new(q, q.shape, bf)
         if return_k and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            _used_on(stream, k_out)
-        rc = lib().kv_append(_ptr(q), _ptr(k), _ptr(v), strides, _ptr(positions),
-                             float(rope_base), int(rope_pairing), _ptr(q_out), _ptr(k_out),
-                             _ptr(slots), _ptr(k_cache), _ptr(v_cache), B, Hq, Hkv, N, d,
-                             page_size, num_pages, _stream(stream))
-    _raise(rc, "kv_append")
+            k_out = on.new(k, shape, bf)
+        rc = lib().kv_append(_data(q), k.data_ptr(), _data(v),
+                             _Strides9(qb, qh, qt, kb, kh, kt, vb, vh, vt), _data(positions),
+                             rope_base, rope_pairing, _data(q_out), _data(k_out), _data(slots),
+                             _data(k_cache), _data(v_cache), B, Hq, Hkv, N, d, page_size,
+                             num_pages, on.raw)
+    if rc != 0:
+        raise AttnError(rc, "kv_append")
     return q_out, k_out
+
+
+_Strides9 = ctypes.c_int64 * 9
 
 
 def attn_tree_workspace_size(B, Hq, Hkv, Nq, d) -> int:
@@ -578,53 +636,70 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
     [B, Hkv, Nk, d] (key_lens None: Nk).  Returns (o, lse) as attn_fwd; rows at
     or beyond new_lens[b] are 0 and -inf."""
     torch = _torch()
-    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (k_new, "k_new"),
-                 (v_new, "v_new")):
-        _check_tensor(t, n, torch.bfloat16, 4)
-    B, Hq, Nq, d = q.shape
-    Hkv = k_new.shape[1]
-    if tuple(k_new.shape) != (B, Hkv, Nq, d) or tuple(v_new.shape) != (B, Hkv, Nq, d):
-        raise ValueError(f"shape mismatch q{tuple(q.shape)} k_new{tuple(k_new.shape)} "
+    bf, i32 = torch.bfloat16, torch.int32
+    _check_tensor(q, "q", bf, 4)
+    _check_tensor(k_new, "k_new", bf, 4)
+    _check_tensor(k_cache, "k_cache", bf, 4)
+    B, Hq, Nq, d = shape = q.shape
+    Bn, Hkv, Nn, dn = new = k_new.shape
+    cs = k_cache.shape
+    if Bn != B or Nn != Nq or dn != d or v_new.shape != new:
+        raise ValueError(f"shape mismatch q{tuple(shape)} k_new{tuple(new)} "
                          f"v_new{tuple(v_new.shape)}")
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or k_cache.shape[1] != Hkv \
-            or k_cache.shape[3] != d:
-        raise ValueError(f"cache shapes {tuple(k_cache.shape)}, {tuple(v_cache.shape)} do not "
-                         f"match k_new{tuple(k_new.shape)}")
+    if v_cache.shape != cs or cs[1] != Hkv or cs[3] != d:
+        raise ValueError(f"cache shapes {tuple(cs)}, {tuple(v_cache.shape)} do not match "
+                         f"k_new{tuple(new)}")
+    args = [(k_cache, "k_cache", bf, cs), (v_cache, "v_cache", bf, cs), (k_new, "k_new", bf, new),
+            (v_new, "v_new", bf, new), (parents, "parents", i32, (B, Nq))]
     max_pages = num_pages = page_size = Nk = 0
     if block_table is not None:
-        _check_tensor(block_table, "block_table", torch.int32, 2)
-        if block_table.shape[0] != B:
-            raise ValueError(f"block_table has {block_table.shape[0]} rows, expected B = {B}")
+        _check_tensor(block_table, "block_table", i32, 2)
+        rows, max_pages = block_table.shape
+        if rows != B:
+            raise ValueError(f"block_table has {rows} rows, expected B = {B}")
         if key_lens is None:
             raise ValueError("attn_fwd_tree over a paged cache needs key_lens")
-        max_pages, num_pages, page_size = block_table.shape[1], k_cache.shape[0], k_cache.shape[2]
+        args.append((block_table, "block_table", i32, (B, max_pages)))
+        num_pages, page_size = cs[0], cs[2]
     else:
-        if k_cache.shape[0] != B:
-            raise ValueError(f"cache has {k_cache.shape[0]} sequences, expected B = {B}")
-        Nk = k_cache.shape[2]
-    _check_shape(parents, "parents", torch.int32, (B, Nq))
+        if cs[0] != B:
+            raise ValueError(f"cache has {cs[0]} sequences, expected B = {B}")
+        Nk = cs[2]
+    if key_lens is not None:
+        _check_tensor(key_lens, "key_lens", i32, 1)
+        if key_lens.numel() != B:
+            raise ValueError(f"key_lens has {key_lens.numel()} entries, expected B = {B}")
+        args.append((key_lens, "key_lens", i32, (B,)))
     if new_lens is not None:
-        _check_shape(new_lens, "new_lens", torch.int32, (B,))
-    _check_workspace(workspace)
-    _check_io(q, key_lens, out, lse if return_lse else None, B, Hq, Nq,
-              extra=[(k_cache, "k_cache"), (v_cache, "v_cache"), (k_new, "k_new"),
-                     (v_new, "v_new"), (parents, "parents"), (new_lens, "new_lens"),
-                     (block_table, "block_table"), (workspace, "workspace")])
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with torch.cuda.device(q.device):
-        made = [out is None, return_lse and lse is None]
-        out, lse = _outputs(q, out, lse, return_lse, B, Hq, Nq)
-        _used_on(stream, *(t for t, m in zip((out, lse), made) if m))
+        args.append((new_lens, "new_lens", i32, (B,)))
+    if out is not None:
+        args.append((out, "out", bf, shape))
+    if not return_lse:
+        lse = None
+    elif lse is not None:
+        args.append((lse, "lse", torch.float32, (B, Hq, Nq)))
+    if workspace is not None:
+        _check_workspace(workspace)
+        args.append((workspace, "workspace", torch.uint8, workspace.shape))
+    with _On(_check_all(q, args), stream) as on:
+        if out is None:
+            out = on.new(q, shape, bf)
+        if return_lse and lse is None:
+            lse = on.new(q, (B, Hq, Nq), torch.float32)
+        L = lib()
         if workspace is None:
-            workspace = _scratch(attn_tree_workspace_size(B, Hq, Hkv, Nq, d), q.device, stream)
-        rc = lib().attn_fwd_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                 max_pages, page_size, num_pages, _ptr(k_new), _ptr(v_new),
-                                 _ptr(parents), _ptr(new_lens), _ptr(out),
-                                 _ptr(lse if return_lse else None), B, Hq, Hkv, Nq, Nk, d,
-                                 float(scale), _ptr(key_lens), _ptr(workspace),
-                                 workspace.numel(), _stream(stream))
-    _raise(rc, "attn_fwd_tree")
+            ws_bytes = L.attn_tree_workspace_size(B, Hq, Hkv, Nq, d)
+            workspace = on.new(q, (max(ws_bytes, 256),), torch.uint8)
+        else:
+            ws_bytes = workspace.numel()
+        rc = L.attn_fwd_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                             _data(block_table), max_pages, page_size, num_pages,
+                             k_new.data_ptr(), v_new.data_ptr(), parents.data_ptr(),
+                             _data(new_lens), out.data_ptr(), _data(lse), B, Hq, Hkv, Nq, Nk, d,
+                             1.0 / math.sqrt(d) if scale is None else scale, _data(key_lens),
+                             workspace.data_ptr(), ws_bytes, on.raw)
+    if rc != 0:
+        raise AttnError(rc, "attn_fwd_tree")
     return (out, lse) if return_lse else out
 
 
