@@ -51,6 +51,14 @@ constexpr int kSegSlots = 4;      // depth of the ring of segments
 constexpr int kSegReaders = 11;   // warps that read it: MMA, 2 Q, 8 softmax
 constexpr float kRescaleLog2 = 8.0f;
 
+// a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division takes
+// some hundred cycles)
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0
+             ? (long long)((unsigned)a / (unsigned)b)
+             : a / b;
+}
+
 // Costs of the work split, in parts of a tile's HBM time: a tile of up to 128
 // rows, one of a pair, and what a unit's start costs.
 constexpr int kCostTile = 5, kCostPair = 8, kCostUnit = 5;
@@ -88,11 +96,23 @@ struct Smem {
 
 struct Args {
   TreeArgs t;
-  float* part_o;      // [2 * grid][RP][D]
-  float* part_lse;    // [2 * grid][RP], log2 units
-  int* meta;          // [grid][8], see the producer
-  int G, RP, grid, oob_row;
+  float* part_o;      // [2 * ranges][RP][D]
+  float* part_lse;    // [2 * ranges][RP], log2 units
+  struct Record* records;   // [ranges]
+  int G, RP, grid, ranges, oob_row;
 };
+
+// What a range leaves for the join: the unit it starts and does not finish.
+struct Record {
+  int last;           // range that holds the unit's last tile; -1: no such unit
+  int slot;           // its partial slot here; it is 2 * range in those after
+  int b, h, rg, rows, nb;   // the unit and its rows
+  int w, nt, pad;     // its tiles and their cost
+  long long p0;       // where it starts
+  long long T;        // total cost
+  long long pad2;
+};
+static_assert(sizeof(Record) == 64, "copied in 16-byte pieces");
 
 // A segment as its readers see it.
 struct Seg {
@@ -125,15 +145,33 @@ struct Split {
   }
   __device__ __forceinline__ int weight(int rg) const { return rg < nrg - 1 ? kCostPair : w_last; }
   __device__ __forceinline__ long long unit(int w) const { return kCostUnit + (long long)nt * w; }
-  // where tile j of a unit starts (the unit's own cost belongs to tile 0)
-  static __device__ __forceinline__ long long tile_at(int j, int w) {
-    return j == 0 ? 0 : kCostUnit + (long long)j * w;
-  }
-  // tiles of a unit that start before x
-  __device__ __forceinline__ int tiles_before(long long x, int w) const {
-    if (x <= 0) return 0;
-    const long long j = (x - kCostUnit + w - 1) / w;   // (truncation: <= 0 below the unit cost)
-    return j < 1 ? 1 : (j > nt ? nt : (int)j);
+};
+
+// Where tile j of a unit starts (the unit's own cost belongs to tile 0), and how
+// many of its nt tiles start before x.
+__device__ __forceinline__ long long tile_at(int j, int w) {
+  return j == 0 ? 0 : kCostUnit + (long long)j * w;
+}
+__device__ __forceinline__ int tiles_before(long long x, int w, int nt) {
+  if (x <= 0) return 0;
+  x -= kCostUnit;
+  if (x <= 0) return 1;
+  const long long j = div_pos(x + w - 1, w);
+  return j > nt ? nt : (int)j;
+}
+
+// The cuts: range i is [at(i), at(i + 1)) of the total cost.
+struct Cuts {
+  long long T;
+  int n;
+  __device__ __forceinline__ Cuts(long long total, const Args& a) : T(total), n(a.ranges) {}
+  __device__ __forceinline__ long long at(int i) const { return div_pos(T * i, n); }
+  // the range that holds x
+  __device__ __forceinline__ int of(long long x) const {
+    int c = (int)div_pos(x * n, T);
+    while (c + 1 < n && at(c + 1) <= x) ++c;
+    while (c > 0 && at(c) > x) --c;
+    return c;
   }
 };
 
@@ -179,6 +217,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
   const TreeArgs& t = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // the join may launch now; it waits for this grid before it reads anything
   asm volatile("griddepcontrol.launch_dependents;");
   if ((smem_u32(smem) & 1023u) != 0) {   // (never seen; nothing below would be in place)
     atomicExch(&g_device_status, (int)ATTN_ECUDA);
@@ -227,7 +266,8 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     if (w < warp) before += scan[w];
     T += scan[w];
   }
-  const long long start = T * blockIdx.x / a.grid, end = T * (blockIdx.x + 1) / a.grid;
+  const Cuts cuts(T, a);
+  const long long start = cuts.at(blockIdx.x), end = cuts.at(blockIdx.x + 1);
   long long at = before + incl - mine;
   if (start < end && at <= start && start < at + mine) {
     for (int b = b_lo; b < b_hi; ++b) {
@@ -277,7 +317,9 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     int k = 0, g = 0;        // segments and ring positions so far
     int armed = 0;           // ring positions whose barrier was armed (for the drain)
     bool ok = true;
-    int meta_mid = 0, meta_c1 = -1, meta_slot = 0, meta_b = 0, meta_h = 0, meta_rg = 0;
+    Record rec;
+    rec.last = -1;
+    rec.T = T;
     int b = 0, h = 0, rg = 0, j0 = 0, Lb = 0, nb = 0;
     long long p0 = 0;        // where the current unit starts
     Split sp(0, 0, 1);
@@ -307,19 +349,19 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       b = (int)scan[12];
       load_seq();
       long long rel = start - scan[13];
-      h = (int)(rel / sp.head);
+      h = (int)div_pos(rel, sp.head);
       rel -= h * sp.head;
-      rg = (int)(rel / sp.unit(kCostPair));
+      rg = (int)div_pos(rel, sp.unit(kCostPair));
       if (rg > sp.nrg - 1) rg = sp.nrg - 1;
       rel -= rg * sp.unit(kCostPair);
       p0 = start - rel;
-      j0 = rel == 0 ? 0 : sp.tiles_before(rel, sp.weight(rg));
+      j0 = rel == 0 ? 0 : tiles_before(rel, sp.weight(rg), sp.nt);
       if (j0 == sp.nt) next_unit();
     }
     while (ok) {
       const int w = sp.weight(rg);
       int n = 0;
-      if (more && b < t.B && p0 + Split::tile_at(j0, w) < end) n = sp.tiles_before(end - p0, w) - j0;
+      if (more && b < t.B && p0 + tile_at(j0, w) < end) n = tiles_before(end - p0, w, sp.nt) - j0;
       const int slot = k % kSegSlots;
       if (!mbar_wait_warp(&bars[L::SEG_EMPTY + slot], ((k / kSegSlots) & 1) ^ 1, abort_flag)) break;
       const bool whole = j0 == 0 && n == sp.nt;
@@ -330,15 +372,13 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
         mbar_arrive(&bars[L::SEG_FULL + slot]);
       }
       if (n == 0) break;
-      if (k == 0 && j0 > 0) meta_mid = 1;
       if (j0 == 0 && n < sp.nt) {   // this CTA starts a unit that others finish
-        const long long x = p0 + Split::tile_at(sp.nt - 1, w);
-        long long c = x * a.grid / T;
-        while (c + 1 < a.grid && T * (c + 1) / a.grid <= x) ++c;
-        while (c > 0 && T * c / a.grid > x) --c;
-        meta_c1 = (int)c;
-        meta_slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
-        meta_b = b; meta_h = h; meta_rg = rg;
+        const int rows = a.G * nb - rg * 2 * kTile;
+        rec.last = cuts.of(p0 + tile_at(sp.nt - 1, w));
+        rec.slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
+        rec.b = b; rec.h = h; rec.rg = rg;
+        rec.rows = rows < 2 * kTile ? rows : 2 * kTile;
+        rec.nb = nb; rec.w = w; rec.nt = sp.nt; rec.p0 = p0;
       }
       ++k;
 
@@ -410,9 +450,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       if (j0 == sp.nt - 1) next_unit(); else more = false;
     }
     if (lane == 0) {
-      int* m = a.meta + 8 * blockIdx.x;
-      m[0] = meta_mid; m[1] = meta_c1; m[2] = meta_slot;
-      m[3] = meta_b; m[4] = meta_h; m[5] = meta_rg;
+      a.records[blockIdx.x] = rec;
       // every issued load must land before the CTA may exit
       for (int j = armed - NS > 0 ? armed - NS : 0; j < armed; ++j)
         mbar_wait(&bars[L::FULL + j % NS], (j / NS) & 1, nullptr);
@@ -506,12 +544,13 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       const int dg = kStep / s.nb, di = kStep % s.nb;
       const __nv_bfloat16* qb =
           t.q + ((size_t)s.b * t.Hq + (size_t)s.h * a.G) * t.Nq * D + c * 8;
-      for (int sl = 0; sl < nq; ++sl, ++qt) {
-        if (!mbar_wait_warp(&bars[L::Q_EMPTY + (qt & 1)], ((qt >> 1) & 1) ^ 1, abort_flag)) {
+      for (int sl = 0; sl < nq; ++sl) {
+        const int buf = (qt + sl) & 1;
+        if (!mbar_wait_warp(&bars[L::Q_EMPTY + buf], (((qt + sl) >> 1) & 1) ^ 1, abort_flag)) {
           ok = false;
           break;
         }
-        const uint32_t dst = smem_u32(smem + L::kQ + (qt & 1) * L::kTileBytes) +
+        const uint32_t dst = smem_u32(smem + L::kQ + buf * L::kTileBytes) +
                              (uint32_t)(c >> 3) * L::kBox;
         int r = (warp - 10) * 64 + lane / kChunks;
         const int r_end = (warp - 10) * 64 + 64, r0 = s.rg * 2 * kTile + sl * kTile;
@@ -522,12 +561,18 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
           i += di;
           if (i >= s.nb) { i -= s.nb; ++gh; }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      for (int sl = 0; ok && sl < nq; ++sl) {   // (the second tile's rows are on their way too)
+        if (sl + 1 < nq) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::Q_FULL + (qt & 1)]);
+        if (lane == 0) mbar_arrive(&bars[L::Q_FULL + ((qt + sl) & 1)]);
       }
+      qt += nq;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // rows of the nodes a sequence does not have
     if (t.new_lens) {
       for (long long x = blockIdx.x * 2 + (warp - 10); x < (long long)t.B * t.Hq; x += a.grid * 2) {
@@ -800,10 +845,13 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
               for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + 8 * q) = v[q];
             }
           } else if (store) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+            float* dst = a.part_o + prow * D + 32 * c;
+            auto u4 = [&](int q) {
+              return make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
+                                __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3]));
+            };
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) st_global_32B(dst + 8 * q, u4(2 * q), u4(2 * q + 1));
           }
         }
       }
@@ -828,80 +876,113 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
   }
 }
 
-// Joins the partial results of the units that cross a cut: blockIdx.x = the CTA
-// in which the unit starts, blockIdx.y = a chunk of its rows.  The parts' log-
-// sum-exps of the chunk's rows go to shared memory; a thread then merges four
-// columns of one row over the parts, in order.
-constexpr int kJoinThreads = 256;
+// Joins the partial results of the units that cross a cut: blockIdx.x = the
+// range in which the unit starts, blockIdx.y = a chunk of its rows, 4 rows a
+// warp.  Four parts at a time, in the order of the keys: all their columns are
+// asked for first, then a lane loads the log-sum-exp of one (part, row) and
+// makes its weight under a running maximum.  Bound by latency (the record, then
+// the partial results, then the store) and, with 256 rows, by how many partial
+// results (up to 128 KB a part, out of L2) are on their way at once.
+constexpr int kJoinWarps = 4, kJoinRows = 4, kJoinParts = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(tr::Args a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(tr::Args a) {
   using namespace tr;
-  asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int HB = kJoinThreads * 4 / D;    // rows of a chunk
-  extern __shared__ float js[];               // float [parts][HB], then int [parts]
-  __shared__ int s_np;
-  int* slots = reinterpret_cast<int*>(js + (size_t)a.grid * HB);
+  constexpr int E = D / 32;
   const TreeArgs& t = a.t;
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x, r0 = (blockIdx.y * kJoinWarps + warp) * kJoinRows;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int* m = a.meta + 8 * c0;
-  const int c1 = m[1];
-  if (c1 < 0) return;
-  const int b = m[3], h = m[4], rg = m[5];
-  const int nb = live_nodes(t, b);
-  int rows = a.G * nb - rg * 2 * kTile;
-  if (rows > 2 * kTile) rows = 2 * kTile;
-  const int r0 = blockIdx.y * HB;
-  if (r0 >= rows) return;
-  if (threadIdx.x < 32) {
-    // the starting CTA's part, then those of the CTAs whose first segment
-    // continues the unit (a CTA without a tile has none)
-    int cnt = 1;
-    if (lane == 0) slots[0] = m[2];
-    for (int base = c0 + 1; base <= c1; base += 32) {
-      const int c = base + lane;
-      const bool has = c <= c1 && a.meta[8 * c] != 0;
-      const unsigned bal = __ballot_sync(0xffffffffu, has);
-      if (has) slots[cnt + __popc(bal & ((1u << lane) - 1))] = 2 * c;
-      cnt += __popc(bal);
+  const Record u = a.records[c0];
+  if (u.last < 0 || r0 >= u.rows) return;
+  const int nr = u.rows - r0 < kJoinRows ? u.rows - r0 : kJoinRows;
+  const Cuts cuts(u.T, a);
+  const int lp = lane / kJoinRows, lr = lane % kJoinRows;   // this lane's part and row of a batch
+  float m = -INFINITY, sum = 0.f;      // of row lr, the same in every lane group
+  float acc[kJoinRows][E];
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+  for (int base = c0; base <= u.last; base += 32) {
+    // ranges that hold a tile of the unit (a short one may hold none)
+    const int c = base + lane;
+    bool has = c <= u.last;
+    if (has && c > c0)
+      has = tiles_before(cuts.at(c + 1) - u.p0, u.w, u.nt) > tiles_before(cuts.at(c) - u.p0, u.w, u.nt);
+    unsigned bal = __ballot_sync(0xffffffffu, has);
+    while (bal) {
+      const int n = __popc(bal) < kJoinParts ? __popc(bal) : kJoinParts;
+      float v[kJoinParts][kJoinRows][E];
+      int ms = 0;
+#pragma unroll
+      for (int k = 0; k < kJoinParts; ++k) {
+        const int ci = base + __ffs(bal) - 1;
+        bal &= bal - 1;
+        const int slot = ci == c0 ? u.slot : 2 * ci;
+        ms = lp == k ? slot : ms;
+        const float* src = a.part_o + ((size_t)slot * a.RP + r0) * D + lane * E;
+#pragma unroll
+        for (int i = 0; i < kJoinRows; ++i) {
+          const bool ld = k < n && i < nr;
+          if constexpr (E == 4)
+            *reinterpret_cast<float4*>(v[k][i]) =
+                ld ? *reinterpret_cast<const float4*>(src + i * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+          else
+            *reinterpret_cast<float2*>(v[k][i]) =
+                ld ? *reinterpret_cast<const float2*>(src + i * D) : make_float2(0.f, 0.f);
+        }
+      }
+      const float ls = lp < n && lr < nr ? a.part_lse[(size_t)ms * a.RP + r0 + lr] : -INFINITY;
+      float mx = fmaxf(m, ls);
+#pragma unroll
+      for (int o = kJoinRows; o < kJoinRows * kJoinParts; o <<= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float f = m == -INFINITY ? 0.f : exp2_approx(m - mx);
+      const float w = ls == -INFINITY ? 0.f : exp2_approx(ls - mx);
+      float ws = w;
+#pragma unroll
+      for (int o = kJoinRows; o < kJoinRows * kJoinParts; o <<= 1)
+        ws += __shfl_xor_sync(0xffffffffu, ws, o);
+      sum = sum * f + ws;
+      m = mx;
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] *= fi;
+#pragma unroll
+        for (int k = 0; k < kJoinParts; ++k) {
+          const float wi = __shfl_sync(0xffffffffu, w, k * kJoinRows + i);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[i][e] = fmaf(wi, v[k][i][e], acc[i][e]);
+        }
+      }
     }
-    if (lane == 0) s_np = cnt;
-  }
-  __syncthreads();
-  const int np = s_np;
-  for (int x = threadIdx.x; x < np * HB; x += kJoinThreads) {
-    const int p = x / HB, r = r0 + x % HB;
-    js[x] = r < rows ? a.part_lse[(size_t)slots[p] * a.RP + r] : -INFINITY;
-  }
-  __syncthreads();
-  const int lr = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-  const int r = r0 + lr;
-  if (r >= rows) return;
-  float mx = -INFINITY, sum = 0.f;
-  for (int p = 0; p < np; ++p) mx = fmaxf(mx, js[p * HB + lr]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = 0; p < np; ++p) {
-    const float ls = js[p * HB + lr];
-    const float w = ls == -INFINITY ? 0.f : exp2_approx(ls - mx);
-    const float4 v =
-        *reinterpret_cast<const float4*>(a.part_o + ((size_t)slots[p] * a.RP + r) * D + col);
-    sum += w;
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int rr = rg * 2 * kTile + r;
-  const int head = rr / nb;
-  const size_t row = ((size_t)b * t.Hq + (size_t)h * a.G + head) * t.Nq + (rr - head * nb);
-  uint2 o;
-  o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-  o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(t.o + row * D + col) = o;
-  if (t.lse && col == 0) t.lse[row] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * kLn2;
+  const int rr = u.rg * 2 * kTile + r0;
+  int head = rr / u.nb, node = rr - head * u.nb;
+  const size_t unit = (size_t)u.b * t.Hq + (size_t)u.h * a.G;
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i) {
+    const float fi = __shfl_sync(0xffffffffu, inv, i);
+    if (i < nr) {
+      const size_t row = (unit + head) * t.Nq + node;
+      uint32_t* o = reinterpret_cast<uint32_t*>(t.o + row * D + lane * E);
+      if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[i][0] * fi, acc[i][1] * fi),
+                                                  pack_bf16x2(acc[i][2] * fi, acc[i][3] * fi));
+      else
+        *o = pack_bf16x2(acc[i][0] * fi, acc[i][1] * fi);
+      if (t.lse && lane == i) t.lse[row] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
+    }
+    if (++node == u.nb) {
+      node = 0;
+      ++head;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -927,9 +1008,9 @@ int launch_tree_t(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& t
   const int rc = launch_programmatic(kern, dim3(a.grid), dim3(tr::kThreads), smem, st, tk, tv, tkn,
                                      tvn, a);
   if (rc != ATTN_OK) return rc;
-  constexpr int HB = kJoinThreads * 4 / D;
-  return launch_programmatic(tree_join_kernel<D>, dim3(a.grid, (a.RP + HB - 1) / HB),
-                             dim3(kJoinThreads), (size_t)a.grid * (HB + 1) * 4, st, a);
+  constexpr int HB = kJoinWarps * kJoinRows;
+  return launch_programmatic(tree_join_kernel<D>, dim3(a.ranges, (a.RP + HB - 1) / HB),
+                             dim3(kJoinWarps * 32), 0, st, a);
 }
 }  // namespace
 
@@ -937,7 +1018,7 @@ size_t tree_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int num_sms) 
   (void)B;
   const size_t rp = (size_t)rows_per_slot(Hq, Hkv, Nq), slots = 2 * (size_t)num_sms;
   return round256(slots * rp * d * sizeof(float)) + round256(slots * rp * sizeof(float)) +
-         round256((size_t)num_sms * 8 * sizeof(int));
+         round256((size_t)num_sms * sizeof(tr::Record));
 }
 
 int launch_tree(const TreeArgs& t, int d, void* workspace, int num_sms, cudaStream_t st) {
@@ -952,7 +1033,8 @@ int launch_tree(const TreeArgs& t, int d, void* workspace, int num_sms, cudaStre
   w += round256(slots * a.RP * d * sizeof(float));
   a.part_lse = reinterpret_cast<float*>(w);
   w += round256(slots * a.RP * sizeof(float));
-  a.meta = reinterpret_cast<int*>(w);
+  a.records = reinterpret_cast<tr::Record*>(w);
+  a.ranges = num_sms;
   // the drafts [B * Hkv, Nq, d] and a contiguous cache [B * Hkv, Nk, d] in
   // boxes of 128 rows x 64 columns; a paged cache page by page
   CUtensorMap tk, tv, tkn, tvn;
