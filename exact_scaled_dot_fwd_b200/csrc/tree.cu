@@ -18,8 +18,10 @@
 // Warp roles (12 warps):
 //   0-3, 4-7   softmax of slot 0 and of slot 1 (a thread owns a TMEM lane)
 //   8          tcgen05.mma issuer, TMEM allocator
-//   9          producer: cuts the segments, loads K and V tiles by TMA
-//   10-11      load Q rows (gathered, so cp.async), clear the dead output rows
+//   9          cuts the segments, loads K tiles by TMA
+//   10         loads Q rows (gathered, so cp.async), clears the dead output rows
+//   11         loads V tiles by TMA (a box takes a warp some 100 cycles, and 16-token
+//              pages make 16 boxes of a tile's K and V)
 // Steps of a segment alternate between the two slots (TMEM: S0 S1 O0 O1):
 //   row group above 128 rows ("pair"): slot t holds rows 128 t .. of it and
 //     each key tile is taken by both slots in turn;
@@ -36,6 +38,8 @@
 // maxima and O stay in fp32.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -48,7 +52,7 @@ constexpr int kTile = 128;        // keys per tile, rows per slot
 constexpr int kThreads = 384;
 constexpr int kMaxB = 2048;
 constexpr int kSegSlots = 4;      // depth of the ring of segments
-constexpr int kSegReaders = 11;   // warps that read it: MMA, 2 Q, 8 softmax
+constexpr int kSegReaders = 11;   // warps that read it: MMA, Q, V, 8 softmax
 constexpr float kRescaleLog2 = 8.0f;
 
 // a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division takes
@@ -75,11 +79,11 @@ struct Smem {
   enum {
     FULL = 0,
     EMPTY = FULL + NS,
-    Q_FULL = EMPTY + NS,      // [2], 2 arrivals
+    Q_FULL = EMPTY + NS,      // [2]
     Q_EMPTY = Q_FULL + 2,     // [2]
-    S_FULL = Q_EMPTY + 2,     // [2]
-    P_FULL = S_FULL + 2,      // [2], 128 arrivals
-    O_FULL = P_FULL + 2,      // [2]
+    S_FULL = Q_EMPTY + 2,     // [3]
+    P_FULL = S_FULL + 3,      // [3], 128 or 256 arrivals
+    O_FULL = P_FULL + 3,      // [2]
     SEG_FULL = O_FULL + 2,    // [kSegSlots]
     SEG_EMPTY = SEG_FULL + kSegSlots,   // [kSegSlots], kSegReaders arrivals
     MMA_DONE = SEG_EMPTY + kSegSlots,
@@ -90,7 +94,8 @@ struct Smem {
   static constexpr int kScan = kSeg + kSegSlots * kSegInts * 4;   // long long [16]
   static constexpr int kTmemSlot = kScan + 16 * 8;
   static constexpr int kAbort = kTmemSlot + 8;
-  static constexpr int kTotal = kAbort + 8;   // (the base is 1024-byte aligned)
+  static constexpr int kArmed = kAbort + 8;       // int [NS]: the position each stage was last filled for
+  static constexpr int kTotal = kArmed + NS * 4;   // (the base is 1024-byte aligned)
   static_assert(kTotal <= 232448, "shared memory over the 227 KB per-CTA limit");
 };
 
@@ -197,13 +202,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 }  // namespace tr
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, int kKeys>
 __global__ void __launch_bounds__(tr::kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                    const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn,
                    tr::Args a) {
   using namespace tr;
   using L = Smem<D>;
+  constexpr bool kWide = kKeys == 0;
+  constexpr int kCopies = kWide ? 1 : 64 / kKeys;   // of the rows in a row tile
   constexpr int NS = L::NS;
   constexpr uint32_t kIdescS = tc::idesc_bf16(kTile, kTile, false, false);
   constexpr uint32_t kIdescPV = tc::idesc_bf16(kTile, D, false, true);
@@ -214,6 +221,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
   long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  volatile int* armed = reinterpret_cast<volatile int*>(smem + L::kArmed);
   const TreeArgs& t = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -226,12 +234,13 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NUM_BARS; ++i) {
       uint32_t c = 1;
-      if (i == L::P_FULL || i == L::P_FULL + 1) c = 128;
-      if (i == L::Q_FULL || i == L::Q_FULL + 1) c = 2;
+      if (i >= L::P_FULL && i < L::O_FULL) c = kWide ? 128 : 256;
+      if (!kWide && (i == L::Q_EMPTY || i == L::Q_EMPTY + 1)) c = 8;
       if (i >= L::SEG_EMPTY && i < L::SEG_EMPTY + kSegSlots) c = kSegReaders;
       mbar_init(&bars[i], c);
     }
     *abort_flag = 0;
+    for (int i = 0; i < NS; ++i) armed[i] = -1;
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -300,10 +309,66 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     return r < 2 * kTile ? r : 2 * kTile;
   };
   // Ring positions of a segment of n tiles that starts at g.  Pair: K0 V0 K1
-  // V1 ..; else K0 K1 V0 K2 V1 ..: the order in which the MMAs use them.
-  auto k_pos = [](int g, int j, bool pair) { return pair ? g + 2 * j : (j == 0 ? g : g + 2 * j - 1); };
+  // V1 ..; else the first kAhead K, then V0 and the next K, V1 and the next
+  // K, ..: the order in which the MMAs use them.
+  constexpr int kAhead = kWide ? 2 : 3;
+  auto k_pos = [](int g, int j, bool pair) {
+    return pair ? g + 2 * j : (j < kAhead ? g + j : g + 2 * j - kAhead + 1);
+  };
   auto v_pos = [](int g, int j, int n, bool pair) {
-    return pair ? g + 2 * j + 1 : (j < n - 1 ? g + 2 * j + 2 : g + 2 * n - 1);
+    return pair ? g + 2 * j + 1 : (j <= n - kAhead ? g + kAhead + 2 * j : g + n + j);
+  };
+
+  // The K or the V tiles of a segment into their ring positions, by one warp.
+  auto load_tiles = [&](const Seg& s, int g, bool is_v) -> bool {
+    const int n = s.n, np = s.np();
+    const bool pair = kWide && group_rows(s) > kTile;
+    const int bh = s.b * t.Hkv + s.h;
+    const int npg = kPaged ? kTile / t.page_size : 0;
+    const int32_t* table = kPaged ? t.block_table + (size_t)s.b * t.max_pages : nullptr;
+    const CUtensorMap* map = is_v ? &tv : &tk;
+    const CUtensorMap* map_new = is_v ? &tvn : &tkn;
+    // this lane's entry of the block table for tile j (-1: a page past the
+    // cached keys), looked up two tiles before it is needed
+    auto entry = [&](int j) -> int {
+      const int pg = (s.j0 + j) * npg + lane;
+      return j < n && lane < npg && pg * t.page_size < s.L ? table[pg] : -1;
+    };
+    int e0 = kPaged ? entry(0) : 0, e1 = kPaged ? entry(1) : 0;
+    for (int j = 0; j < n; ++j) {
+      const int e2 = kPaged ? entry(j + 2) : 0;
+      const int jt = s.j0 + j, pos = is_v ? v_pos(g, j, n, pair) : k_pos(g, j, pair);
+      const int st = pos % NS;
+      uint64_t* full = &bars[L::FULL + st];
+      bool w_ok = true;
+      if (lane == 0) {
+        w_ok = mbar_wait(&bars[L::EMPTY + st], ((pos / NS) & 1) ^ 1, abort_flag);
+        if (w_ok) {
+          mbar_arrive_expect_tx(full, L::kTileBytes);
+          armed[st] = pos;
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, w_ok, 0)) return false;
+      uint8_t* dst = smem + L::kKV + st * L::kTileBytes;
+      if (jt >= np) {
+        if (lane < D / 64)
+          tma_load_3d(dst + lane * L::kBox, map_new, lane * 64, (jt - np) * kTile, bh, full);
+      } else if constexpr (kPaged) {
+        if (lane < npg) {
+          // (pages past the cached keys: the row past the cache, zeros)
+          const int row = (jt * npg + lane) * t.page_size < s.L
+                              ? paged_cache_row(e0, t.num_pages, t.Hkv, s.h, t.page_size, a.oob_row)
+                              : a.oob_row;
+          if constexpr (D == 128) tma_load_4d(dst + lane * t.page_size * 256, map, row >> 3, full);
+          else tma_load_2d(dst + lane * t.page_size * 128, map, 0, row, full);
+        }
+      } else {
+        if (lane < D / 64) tma_load_3d(dst + lane * L::kBox, map, lane * 64, jt * kTile, bh, full);
+      }
+      e0 = e1;
+      e1 = e2;
+    }
+    return true;
   };
 
   if (warp == 9) {
@@ -315,7 +380,6 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       tma_prefetch_desc(&tvn);
     }
     int k = 0, g = 0;        // segments and ring positions so far
-    int armed = 0;           // ring positions whose barrier was armed (for the drain)
     bool ok = true;
     Record rec;
     rec.last = -1;
@@ -382,79 +446,79 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       }
       ++k;
 
-      const int np = (Lb + kTile - 1) / kTile;
-      const int rows = a.G * nb - rg * 2 * kTile;
-      const bool pair = rows > kTile;
-      const int bh = b * t.Hkv + h;
-      const int npg = kPaged ? kTile / t.page_size : 0;
-      const int32_t* table = kPaged ? t.block_table + (size_t)b * t.max_pages : nullptr;
-      // cache row of this lane's page of tile j (the row past the cache,
-      // which the TMA fills with zeros, for pages past the cached keys)
-      auto page_row = [&](int j) -> int {
-        const int pg = j * npg + lane;
-        return (lane < npg && j < np && pg * t.page_size < Lb)
-                   ? paged_cache_row(table[pg], t.num_pages, t.Hkv, h, t.page_size, a.oob_row)
-                   : a.oob_row;
-      };
-      // one K or V tile into ring position pos
-      auto load = [&](int pos, int j, int row, bool is_v) -> bool {
-        const int st = pos % NS;
-        bool w_ok = true;
-        if (lane == 0) {
-          w_ok = mbar_wait(&bars[L::EMPTY + st], ((pos / NS) & 1) ^ 1, abort_flag);
-          if (w_ok) mbar_arrive_expect_tx(&bars[L::FULL + st], L::kTileBytes);
-        }
-        if (!__shfl_sync(0xffffffffu, w_ok, 0)) return false;
-        ++armed;
-        uint8_t* dst = smem + L::kKV + st * L::kTileBytes;
-        if (j >= np) {
-          if (lane < D / 64)
-            tma_load_3d(dst + lane * L::kBox, is_v ? &tvn : &tkn, lane * 64, (j - np) * kTile, bh,
-                        &bars[L::FULL + st]);
-        } else if constexpr (kPaged) {
-          if (lane < npg) {
-            if constexpr (D == 128)
-              tma_load_4d(dst + lane * t.page_size * 256, is_v ? &tv : &tk, row >> 3,
-                          &bars[L::FULL + st]);
-            else
-              tma_load_2d(dst + lane * t.page_size * 128, is_v ? &tv : &tk, 0, row,
-                          &bars[L::FULL + st]);
-          }
-        } else {
-          if (lane < D / 64)
-            tma_load_3d(dst + lane * L::kBox, is_v ? &tv : &tk, lane * 64, j * kTile, bh,
-                        &bars[L::FULL + st]);
-        }
-        return true;
-      };
-      int r_cur = kPaged ? page_row(j0) : 0, r_next = r_cur;
-      if (pair) {
-        for (int j = 0; ok && j < n; ++j) {
-          r_next = kPaged && j + 1 < n ? page_row(j0 + j + 1) : 0;
-          ok = load(g + 2 * j, j0 + j, r_cur, false) && load(g + 2 * j + 1, j0 + j, r_cur, true);
-          r_cur = r_next;
-        }
-      } else {
-        ok = load(g, j0, r_cur, false);
-        r_next = kPaged && n > 1 ? page_row(j0 + 1) : 0;
-        for (int j = 0; ok && j < n; ++j) {
-          const int r2 = kPaged && j + 2 < n ? page_row(j0 + j + 2) : 0;
-          if (j + 1 < n) ok = load(k_pos(g, j + 1, false), j0 + j + 1, r_next, false);
-          if (ok) ok = load(v_pos(g, j, n, false), j0 + j, r_cur, true);
-          r_cur = r_next;
-          r_next = r2;
-        }
-      }
+      Seg sg;
+      sg.b = b; sg.h = h; sg.rg = rg; sg.j0 = j0; sg.n = n; sg.L = Lb; sg.nb = nb;
+      ok = load_tiles(sg, g, false);
       g += 2 * n;
       j0 += n - 1;   // (only its being the unit's last tile matters below)
       if (j0 == sp.nt - 1) next_unit(); else more = false;
     }
     if (lane == 0) {
       a.records[blockIdx.x] = rec;
-      // every issued load must land before the CTA may exit
-      for (int j = armed - NS > 0 ? armed - NS : 0; j < armed; ++j)
-        mbar_wait(&bars[L::FULL + j % NS], (j / NS) & 1, nullptr);
     }
+  } else if (!kWide && warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    // One slot: S of tile u (counted over the segments) in buffer u % 3, three
+    // tiles ahead of P V, O behind them.
+    const uint32_t q_base = smem_u32(smem + L::kQ), kv_base = smem_u32(smem + L::kKV);
+    auto commit = [&](int bar) {
+      if (elect_one()) tc::commit(&bars[bar]);
+      __syncwarp();
+    };
+    int k = 0, g = 0, qt = 0, u0 = 0;
+    bool ok = true;
+    Seg s;
+    while (ok && next_seg(k, s)) {
+      const int n = s.n, np = s.np();
+      auto grouped = [&](int j) { return kPaged && D == 128 && s.j0 + j < np; };
+      auto do_s = [&](int j) -> bool {
+        const int pos = k_pos(g, j, false), buf = (u0 + j) % 3;
+        if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) return false;
+        tc::fence_after();
+        const uint32_t half = grouped(j) ? 1024u : (uint32_t)L::kBox;
+        const uint64_t dq = tc::smem_desc_sw128(q_base + (qt & 1) * L::kTileBytes, 16, 1024);
+        const uint64_t dk = tc::smem_desc_sw128(kv_base + (pos % NS) * L::kTileBytes, 16,
+                                                grouped(j) ? 2048 : 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ss(tmem + 128u * buf, dq + (uint64_t)(((kk >> 2) * L::kBox + (kk & 3) * 32) >> 4),
+                       dk + (uint64_t)(((kk >> 2) * half + (kk & 3) * 32) >> 4), kIdescS,
+                       kk > 0 ? 1u : 0u);
+          tc::commit(&bars[L::S_FULL + buf]);
+          tc::commit(&bars[L::EMPTY + pos % NS]);
+        }
+        __syncwarp();
+        return true;
+      };
+      if (!mbar_wait_warp(&bars[L::Q_FULL + (qt & 1)], (qt >> 1) & 1, abort_flag)) break;
+      for (int j = 0; ok && j < kAhead && j < n; ++j) ok = do_s(j);
+      for (int j = 0; ok && j < n; ++j) {
+        const int u = u0 + j, pos = v_pos(g, j, n, false);
+        if (!mbar_wait_warp(&bars[L::P_FULL + u % 3], (u / 3) & 1, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) { ok = false; break; }
+        tc::fence_after();
+        const uint32_t half = grouped(j) ? 1024u : (uint32_t)L::kBox;
+        const uint32_t grp = grouped(j) ? 2048u : 1024u;
+        const uint64_t dv = tc::smem_desc_sw128(kv_base + (pos % NS) * L::kTileBytes, half, grp);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc::mma_ts(tmem + 384u, tmem + 128u * (u % 3) + kk * 8,
+                       dv + (uint64_t)((kk * 2 * grp) >> 4), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+          tc::commit(&bars[L::O_FULL + (u & 1)]);
+          tc::commit(&bars[L::EMPTY + pos % NS]);
+        }
+        __syncwarp();
+        if (j + kAhead < n) ok = do_s(j + kAhead);
+      }
+      g += 2 * n;
+      u0 += n;
+      ++qt;
+    }
+    // every MMA of this CTA must be complete before TMEM is released
+    commit(L::MMA_DONE);
+    mbar_wait_warp(&bars[L::MMA_DONE], 0, nullptr);
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t q_base = smem_u32(smem + L::kQ), kv_base = smem_u32(smem + L::kKV);
@@ -529,10 +593,18 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     // every MMA of this CTA must be complete before TMEM is released
     commit(L::MMA_DONE);
     mbar_wait_warp(&bars[L::MMA_DONE], 0, nullptr);
-  } else if (warp >= 10) {
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ V tiles
+    int k = 0, g = 0;
+    Seg s;
+    while (next_seg(k, s)) {
+      if (!load_tiles(s, g, true)) break;
+      g += 2 * s.n;
+    }
+  } else if (warp == 10) {
     // ------------------------------------------------------------ Q rows
     // Row r of the unit is node r % nb of head r / nb.  A lane copies chunk
-    // `c` of every (32 / chunks)-th row; the warps take 64 rows of a tile each.
+    // `c` of every (32 / chunks)-th row, to each of the row's copies.
     constexpr int kChunks = D / 8, kStep = 32 / kChunks;
     const int c = lane % kChunks;
     int k = 0, qt = 0;
@@ -540,7 +612,9 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     Seg s;
     while (ok && next_seg(k, s)) {
       const int rows = group_rows(s);
-      const int nq = rows > kTile ? 2 : 1;
+      const int nq = kWide && rows > kTile ? 2 : 1;
+      // (one row tile: all of its 128 lanes hold rows, see the softmax)
+      constexpr int span = kTile / kCopies;
       const int dg = kStep / s.nb, di = kStep % s.nb;
       const __nv_bfloat16* qb =
           t.q + ((size_t)s.b * t.Hq + (size_t)s.h * a.G) * t.Nq * D + c * 8;
@@ -552,11 +626,14 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
         }
         const uint32_t dst = smem_u32(smem + L::kQ + buf * L::kTileBytes) +
                              (uint32_t)(c >> 3) * L::kBox;
-        int r = (warp - 10) * 64 + lane / kChunks;
-        const int r_end = (warp - 10) * 64 + 64, r0 = s.rg * 2 * kTile + sl * kTile;
-        int gh = (r0 + r) / s.nb, i = (r0 + r) % s.nb;
-        for (; r < r_end && sl * kTile + r < rows; r += kStep) {
-          cp_async_16(dst + sw128_offset(r, c & 7), qb + ((size_t)gh * t.Nq + i) * D);
+        const int r0 = s.rg * 2 * kTile + sl * kTile;
+        const int r_end = rows - sl * kTile < span ? rows - sl * kTile : span;
+        int r = lane / kChunks, gh = (r0 + r) / s.nb, i = (r0 + r) % s.nb;
+        for (; r < r_end; r += kStep) {
+          const __nv_bfloat16* src = qb + ((size_t)gh * t.Nq + i) * D;
+#pragma unroll
+          for (int cp = 0; cp < kCopies; ++cp)
+            cp_async_16(dst + sw128_offset(r + cp * span, c & 7), src);
           gh += dg;
           i += di;
           if (i >= s.nb) { i -= s.nb; ++gh; }
@@ -575,13 +652,289 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
     // rows of the nodes a sequence does not have
     if (t.new_lens) {
-      for (long long x = blockIdx.x * 2 + (warp - 10); x < (long long)t.B * t.Hq; x += a.grid * 2) {
+      for (long long x = blockIdx.x; x < (long long)t.B * t.Hq; x += a.grid) {
         const int nb = live_nodes(t, (int)(x / t.Hq));
         uint4* o = reinterpret_cast<uint4*>(t.o + (x * t.Nq + nb) * D);
         for (int e = lane; e < (t.Nq - nb) * (D / 8); e += 32) o[e] = make_uint4(0, 0, 0, 0);
         if (t.lse)
           for (int e = nb + lane; e < t.Nq; e += 32) t.lse[x * t.Nq + e] = -INFINITY;
       }
+    }
+  } else if (!kWide) {
+    // ------------------------------------------------------------ softmax
+    // Both warpgroups take every tile: warps q and q + 4 share the lanes of
+    // quarter q, the one the first 64 keys, the other the last.  With 64 rows or
+    // fewer the lanes hold 2 copies of the rows, with 32 or fewer 4, and copy c
+    // takes the c-th part of either 64 keys: its P is zero elsewhere, its O
+    // row is the sum over its keys, and the copies' maxima and sums are joined
+    // when the segment ends.  So all 8 warps work on any number of rows, 64,
+    // 32 or 16 keys a thread: a tile of 25 rows at d = 64 took 1.13 us with one
+    // warp of each warpgroup on whole rows of every other tile.
+    const int hf = warp >> 2, qr = warp & 3;
+    const int r = qr * 32 + lane;             // TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)(qr * 32) << 16);
+    const float sl2 = t.scale_log2;
+    const bool o_32B = (reinterpret_cast<uintptr_t>(t.o) & 31) == 0;
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
+    int k = 0, g = 0, u0 = 0, qt = 0;
+    bool ok = true;
+    Seg s;
+    bool live = next_seg(k, s);
+    while (!bar_vote_or(1, 256, !live)) {
+      const int rows = group_rows(s), n = s.n, np = s.np();
+      constexpr int copies = kCopies, per_copy = 4 / copies;   // warps
+      const int copy = qr / per_copy;
+      const int lr = (qr - copy * per_copy) * 32 + lane;   // row of the unit
+      const bool idle = lr - lane >= rows;                 // no live row in this warp
+      const bool dead = lr >= rows;                        // computes on anything, is not stored
+      const int rr = lr < rows ? lr : rows - 1;
+      const int head = rr / s.nb, node = rr - head * s.nb;
+      float m_run = -INFINITY, l_run = 0.f;
+
+      // one tile, NC keys of this thread from key k0 of the tile on
+      auto tile = [&](auto mask, int j, int jt, int valid) {
+        constexpr int NC = kWide ? 64 : kKeys;
+        constexpr bool masked = decltype(mask)::value;
+        const int u = u0 + j;
+        const int k0 = 64 * hf + copy * NC;
+        const uint32_t sc = lanes + 128u * (u % 3);
+        unsigned long long seen = ~0ull;                   // bit e: key k0 + e is visible
+        if (masked) {
+          if (jt < np) {
+            const int e = valid - k0;
+            seen = e >= 64 ? ~0ull : (e <= 0 ? 0ull : (1ull << e) - 1ull);
+          } else {
+            // the node and its ancestors among drafts [first, first + NC)
+            const int first = (jt - np) * kTile + k0;
+            const int32_t* par = t.parents + (size_t)s.b * t.Nq;
+            seen = 0ull;
+            for (int v = node; v >= first;) {
+              if (v - first < NC) seen |= 1ull << (v - first);
+              const int p = par[v];
+              if (p < -1 || p >= v) {
+                atomicExch(&g_device_status, (int)ATTN_ERANGE);
+                break;
+              }
+              v = p;
+            }
+          }
+        }
+        // A wait that gives up only clears ok: the warp goes on to the vote, where
+        // it and its partner leave together.
+        if (!mbar_wait_warp(&bars[L::S_FULL + u % 3], (u / 3) & 1, abort_flag)) ok = false;
+        // P V of tile u - 2 (each of its barrier's phases is waited for, in order)
+        if (u >= 2 && !mbar_wait_warp(&bars[L::O_FULL + (u & 1)], ((u - 2) >> 1) & 1, abort_flag))
+          ok = false;
+        tc::fence_after();
+        if (masked && valid < kTile && hf == 0) {
+          // values that do not exist: anything may be stored there
+          const int pos = v_pos(g, j, n, false);
+          if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) ok = false;
+          if (r >= valid) {
+            const bool grouped = kPaged && D == 128 && jt < np;
+            uint8_t* vt = smem + L::kKV + (pos % NS) * L::kTileBytes +
+                          (grouped ? (r >> 3) * 2048 + (r & 7) * 128 : r * 128);
+#pragma unroll
+            for (int hb = 0; hb < D / 64; ++hb)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(vt + hb * (grouped ? 1024 : L::kBox) + c * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (idle) {
+          tc::fence_before();
+          mbar_arrive(&bars[L::P_FULL + u % 3]);
+          return;
+        }
+        // P with the running maximum, which usually stands (O is rescaled only
+        // when a score passes it by more than 8 in log2 units), and the tile's
+        // maximum, from one read of S in chunks of up to 32 scores
+        constexpr int CH = NC < 32 ? NC : 32;
+        uint32_t pk[NC / 2];
+        float rs = 0.f, m_tile = -INFINITY;
+        auto scores = [&](auto want_max, auto want_p) {
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          const float2 c_sl2 = make_float2(sl2, sl2), c_m = make_float2(-mu, -mu);
+          float2 rs2 = make_float2(0.f, 0.f), rs3 = make_float2(0.f, 0.f);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < NC / CH; ++c) {
+            float sv[CH];
+            if constexpr (CH == 16) tc::ld16f(sc + k0 + CH * c, sv); else tc::ld32f(sc + k0 + CH * c, sv);
+            tc::wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < CH; ++e) sv[e] = (seen >> (CH * c + e)) & 1ull ? sv[e] : -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < CH / 2; ++e) {
+              if (decltype(want_max)::value) m4[e & 3] = max3(m4[e & 3], sv[2 * e], sv[2 * e + 1]);
+              if (decltype(want_p)::value) {
+                const float2 y = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), c_sl2, c_m);
+                const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                if (e & 1) rs3 = __fadd2_rn(rs3, p); else rs2 = __fadd2_rn(rs2, p);
+                pk[CH / 2 * c + e] = pack_bf16x2(p.x, p.y);
+              }
+            }
+          }
+          if (decltype(want_max)::value)
+            m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+          rs2 = __fadd2_rn(rs2, rs3);
+          rs = rs2.x + rs2.y;
+        };
+        if (j > 0) scores(std::true_type(), std::true_type());
+        else scores(std::true_type(), std::false_type());
+        // The two threads of a lane agree.  (The vote is also what lets the
+        // second one write its P over scores that the first has read.)
+        const bool need = !dead && m_tile > m_run + kRescaleLog2;
+        if (bar_vote_or(3 + qr, 64, need || j == 0 || !ok)) {
+          ml[hf * kTile + r] = make_float2(m_tile, ok ? 1.f : 0.f);
+          asm volatile("bar.sync %0, 64;" ::"r"(3 + qr) : "memory");
+          const float2 other = ml[(hf ^ 1) * kTile + r];
+          if (!__all_sync(0xffffffffu, ok && other.y != 0.f)) {
+            ok = false;
+            return;
+          }
+          const float m_row = fmaxf(m_tile, other.x);
+          const float m_new = !dead && m_row > m_run + kRescaleLog2 ? m_row : m_run;
+          if (j > 0) {
+            if (!mbar_wait_warp(&bars[L::O_FULL + ((u - 1) & 1)], ((u - 1) >> 1) & 1, abort_flag)) ok = false;
+            tc::fence_after();
+            const float f = (m_new > m_run && m_run != -INFINITY) ? exp2_approx(m_run - m_new) : 1.f;
+            l_run *= f;
+#pragma unroll 1
+            for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {
+              float o[32];
+              tc::ld32f(lanes + 384u + 32 * c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tc::st32f(lanes + 384u + 32 * c, o);
+            }
+          }
+          m_run = m_new;
+          scores(std::false_type(), std::true_type());
+          asm volatile("bar.sync %0, 64;" ::"r"(3 + qr) : "memory");   // (as the vote)
+        }
+        l_run += rs;
+        // keys [64 hf, 64 hf + 64) of P: this copy's, and zeros
+        const uint32_t pc = sc + 32u * hf;
+        if constexpr (NC == 64) {
+          tc::st16(pc, pk);
+          tc::st16(pc + 16, pk + 16);
+        } else {
+          constexpr int W = NC / 2;
+#pragma unroll
+          for (int c = 0; c < 64 / NC; ++c) {
+            uint32_t x[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) x[e] = c == copy ? pk[e] : 0u;
+            if constexpr (W == 16) tc::st16(pc + 16 * c, x); else tc::st8(pc + 8 * c, x);
+          }
+        }
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&bars[L::P_FULL + u % 3]);
+      };
+      for (int j = 0; ok && j < n; ++j) {
+        const int jt = s.j0 + j;                           // tile of the unit
+        const int valid = jt < np ? s.L - jt * kTile : s.nb - (jt - np) * kTile;
+        if (jt >= np || valid < kTile) tile(std::true_type(), j, jt, valid);
+        else tile(std::false_type(), j, jt, valid);
+      }
+      // ---- segment end
+      asm volatile("bar.sync %0, 64;" ::"r"(3 + qr) : "memory");   // (maxima of the last vote read)
+      ml[hf * kTile + r] = make_float2(m_run, l_run);
+      if (ok) {
+        const int u = u0 + n - 1;
+        if (!mbar_wait_warp(&bars[L::O_FULL + (u & 1)], (u >> 1) & 1, abort_flag)) ok = false;
+      }
+      // (also orders the exchange; every softmax thread leaves on the same vote)
+      if (bar_vote_or(2, 256, !ok)) break;
+      tc::fence_after();
+      float m = -INFINITY, l = 0.f;
+      for (int c = 0; c < copies; ++c) m = fmaxf(m, ml[c * per_copy * 32 + lr].x);
+      for (int c = 0; c < copies; ++c) {
+        const float2 x0 = ml[c * per_copy * 32 + lr], x1 = ml[kTile + c * per_copy * 32 + lr];
+        const float lc = x0.y + x1.y;
+        l += x0.x == -INFINITY ? 0.f * lc : lc * exp2_approx(x0.x - m);   // (a NaN stays one)
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float f = (m_run == -INFINITY ? 0.f : exp2_approx(m_run - m)) * inv;
+      const bool direct = (s.flags & 2) != 0;
+      const int slot = 2 * blockIdx.x + ((s.flags & 1) ? 0 : 1);
+      const size_t orow = ((size_t)s.b * t.Hq + (size_t)s.h * a.G + head) * t.Nq + node;
+      const size_t prow = (size_t)slot * a.RP + lr;
+      // the copies are added up through this segment's Q tile, which its MMAs
+      // have read: [half][copy of a pair][32 columns][lanes of a copy]
+      float* ex = reinterpret_cast<float*>(smem + L::kQ + (qt & 1) * L::kTileBytes) +
+                  hf * (L::kTileBytes / 8) + lr;
+      constexpr int span = per_copy * 32;
+#pragma unroll 1
+      for (int c = hf * (D / 64); c < (hf + 1) * (D / 64); ++c) {   // half of the columns
+        float o[32];
+        if (!idle) {
+          tc::ld32f(lanes + 384u + 32 * c, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= f;
+        }
+        for (int half = copies >> 1; half > 0; half >>= 1) {
+          float* x = ex + (copy & (half - 1)) * 32 * span;
+          if (copy >= half && copy < 2 * half) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e * span] = o[e];
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(7 + hf) : "memory");
+          if (copy < half) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] += x[e * span];
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(7 + hf) : "memory");
+        }
+        const bool store = copy == 0 && !dead;
+        if (store && direct) {
+          __nv_bfloat16* dst = t.o + orow * D + 32 * c;
+          uint4 v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q].x = pack_bf16x2(o[8 * q + 0], o[8 * q + 1]);
+            v[q].y = pack_bf16x2(o[8 * q + 2], o[8 * q + 3]);
+            v[q].z = pack_bf16x2(o[8 * q + 4], o[8 * q + 5]);
+            v[q].w = pack_bf16x2(o[8 * q + 6], o[8 * q + 7]);
+          }
+          if (o_32B) {
+            st_global_32B(dst, v[0], v[1]);
+            st_global_32B(dst + 16, v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + 8 * q) = v[q];
+          }
+        } else if (store) {
+          float* dst = a.part_o + prow * D + 32 * c;
+          auto u4 = [&](int q) {
+            return make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
+                              __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3]));
+          };
+#pragma unroll
+          for (int q = 0; q < 4; ++q) st_global_32B(dst + 8 * q, u4(2 * q), u4(2 * q + 1));
+        }
+        __syncwarp();
+      }
+      if (copy == 0 && !dead && hf == 0) {
+        const float lse = l == 0.f ? -INFINITY : m + __log2f(l);
+        if (!direct) a.part_lse[prow] = lse;
+        else if (t.lse) t.lse[orow] = lse * kLn2;
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::Q_EMPTY + (qt & 1)]);
+      g += 2 * n;
+      u0 += n;
+      ++qt;
+      live = next_seg(k, s);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -870,6 +1223,10 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
 
   tc::fence_before();
   __syncthreads();
+  // every load must have landed before the CTA may exit (they all have, unless
+  // a wait gave up)
+  if (warp == 9 && lane < NS && armed[lane] >= 0)
+    mbar_wait(&bars[L::FULL + lane], (armed[lane] / NS) & 1, nullptr);
   if (warp == 8) {
     tc::fence_after();
     tc::dealloc(tmem, 512);
@@ -998,10 +1355,10 @@ int rows_per_slot(int Hq, int Hkv, int Nq) {
 }
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-template <int D, bool kPaged>
-int launch_tree_t(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
+template <int D, bool kPaged, int kKeys>
+int launch_tree_k(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
                   const CUtensorMap& tkn, const CUtensorMap& tvn, cudaStream_t st) {
-  auto kern = tree_tc_kernel<D, kPaged>;
+  auto kern = tree_tc_kernel<D, kPaged, kKeys>;
   constexpr int smem = tr::Smem<D>::kTotal;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return ATTN_ECUDA;
@@ -1011,6 +1368,17 @@ int launch_tree_t(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& t
   constexpr int HB = kJoinWarps * kJoinRows;
   return launch_programmatic(tree_join_kernel<D>, dim3(a.ranges, (a.RP + HB - 1) / HB),
                              dim3(kJoinWarps * 32), 0, st, a);
+}
+
+template <int D, bool kPaged>
+int launch_tree_t(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                  const CUtensorMap& tkn, const CUtensorMap& tvn, cudaStream_t st) {
+  // how many keys of a tile's half a thread takes: the fewer rows, the more
+  // copies of them the 128 lanes hold
+  if (a.RP > 128) return launch_tree_k<D, kPaged, 0>(a, tk, tv, tkn, tvn, st);
+  if (a.RP > 64) return launch_tree_k<D, kPaged, 64>(a, tk, tv, tkn, tvn, st);
+  if (a.RP > 32) return launch_tree_k<D, kPaged, 32>(a, tk, tv, tkn, tvn, st);
+  return launch_tree_k<D, kPaged, 16>(a, tk, tv, tkn, tvn, st);
 }
 }  // namespace
 

@@ -127,6 +127,10 @@ CASES = [
     (6, 6, 6, 2, 64, 8, [4000, 3500, 1290, 3900, 2200, 3000], [2, 2, 1, 2, 0, 2]),
     (4, 24, 6, 33, 128, 32, [2500, 1800, 2100, 40], [33, 32, 9, 33]),   # 132 rows: pairs
     (5, 20, 4, 26, 64, 0, [2500, 1800, 2100, 40, 1], [26, 25, 9, 26, 1]),
+    # enough work for the small ranges that the CTAs take as they get done
+    (4, 16, 8, 2, 128, 64, [8000, 7900, 8100, 7000], [2, 1, 2, 2]),
+    (5, 8, 8, 3, 64, 0, [8000, 7900, 30, 8100, 7000], [3, 2, 3, 0, 1]),
+    (80, 8, 8, 1, 64, 16, [400 + 3 * i for i in range(80)], [1] * 79 + [0]),   # more units than ranges
     (40, 4, 4, 2, 64, 32, [i * 17 % 300 for i in range(40)], [i % 3 for i in range(40)]),
 ]
 
