@@ -20,7 +20,7 @@
 //   8          tcgen05.mma issuer, TMEM allocator
 //   9          cuts the segments, loads K tiles by TMA
 //   10         loads Q rows (gathered, so cp.async), clears the dead output rows
-//   11         loads V tiles by TMA (a box takes a warp some 100 cycles, and 16-token
+//   11         loads V tiles by TMA (with row pairs, warp 10 does; a box takes a warp some 100 cycles, and 16-token
 //              pages make 16 boxes of a tile's K and V)
 // Steps of a segment alternate between the two slots (TMEM: S0 S1 O0 O1):
 //   row group above 128 rows ("pair"): slot t holds rows 128 t .. of it and
@@ -49,10 +49,12 @@ namespace attn {
 namespace tr {
 
 constexpr int kTile = 128;        // keys per tile, rows per slot
-constexpr int kThreads = 384;
+// Row pairs need more registers than 12 warps leave each other (168): one warp
+// less, which loads Q and V in turn.
+constexpr int threads(bool wide) { return wide ? 352 : 384; }
 constexpr int kMaxB = 2048;
 constexpr int kSegSlots = 4;      // depth of the ring of segments
-constexpr int kSegReaders = 11;   // warps that read it: MMA, Q, V, 8 softmax
+constexpr int seg_readers(bool wide) { return wide ? 10 : 11; }   // warps: MMA, Q, V, 8 softmax
 constexpr float kRescaleLog2 = 8.0f;
 
 // a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division takes
@@ -79,20 +81,19 @@ struct Smem {
   enum {
     FULL = 0,
     EMPTY = FULL + NS,
-    Q_FULL = EMPTY + NS,      // [2]
+    Q_FULL = EMPTY + NS,      // [2], 2 arrivals
     Q_EMPTY = Q_FULL + 2,     // [2]
     S_FULL = Q_EMPTY + 2,     // [3]
     P_FULL = S_FULL + 3,      // [3], 128 or 256 arrivals
     O_FULL = P_FULL + 3,      // [2]
     SEG_FULL = O_FULL + 2,    // [kSegSlots]
-    SEG_EMPTY = SEG_FULL + kSegSlots,   // [kSegSlots], kSegReaders arrivals
+    SEG_EMPTY = SEG_FULL + kSegSlots,   // [kSegSlots], seg_readers arrivals
     MMA_DONE = SEG_EMPTY + kSegSlots,
     NUM_BARS = MMA_DONE + 1
   };
   static constexpr int kSeg = kBar + NUM_BARS * 8;   // int [kSegSlots][kSegInts]
   static constexpr int kSegInts = 8;
-  static constexpr int kScan = kSeg + kSegSlots * kSegInts * 4;   // long long [16]
-  static constexpr int kTmemSlot = kScan + 16 * 8;
+  static constexpr int kTmemSlot = kSeg + kSegSlots * kSegInts * 4;
   static constexpr int kAbort = kTmemSlot + 8;
   static constexpr int kArmed = kAbort + 8;       // int [NS]: the position each stage was last filled for
   static constexpr int kTotal = kArmed + NS * 4;   // (the base is 1024-byte aligned)
@@ -203,7 +204,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }  // namespace tr
 
 template <int D, bool kPaged, int kKeys>
-__global__ void __launch_bounds__(tr::kThreads, 1)
+__global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                    const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn,
                    tr::Args a) {
@@ -218,7 +219,6 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   volatile int* segs = reinterpret_cast<volatile int*>(smem + L::kSeg);
-  long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   volatile int* armed = reinterpret_cast<volatile int*>(smem + L::kArmed);
@@ -235,8 +235,9 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     for (int i = 0; i < L::NUM_BARS; ++i) {
       uint32_t c = 1;
       if (i >= L::P_FULL && i < L::O_FULL) c = kWide ? 128 : 256;
+      if (i == L::Q_FULL || i == L::Q_FULL + 1) c = 2;
       if (!kWide && (i == L::Q_EMPTY || i == L::Q_EMPTY + 1)) c = 8;
-      if (i >= L::SEG_EMPTY && i < L::SEG_EMPTY + kSegSlots) c = kSegReaders;
+      if (i >= L::SEG_EMPTY && i < L::SEG_EMPTY + kSegSlots) c = seg_readers(kWide);
       mbar_init(&bars[i], c);
     }
     *abort_flag = 0;
@@ -247,50 +248,13 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     tc::alloc(tmem_slot, 512);
     tc::relinquish();
   }
-  // Launched as a programmatic dependent of the previous kernel in the
-  // stream: nothing in global memory is touched before it has completed.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // ---- total cost, and the sequence in which this CTA's share starts: a
-  // thread sums `per` sequences, the block scans the threads' sums
-  const int per = (t.B + kThreads - 1) / kThreads;
-  const int b_lo = threadIdx.x * per < t.B ? threadIdx.x * per : t.B;
-  const int b_hi = b_lo + per < t.B ? b_lo + per : t.B;
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b)
-    mine += (long long)t.Hkv * Split(cached_len(t, b), live_nodes(t, b), a.G).head;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) scan[warp] = incl;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
-  long long before = 0, T = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    T += scan[w];
-  }
-  const Cuts cuts(T, a);
-  const long long start = cuts.at(blockIdx.x), end = cuts.at(blockIdx.x + 1);
-  long long at = before + incl - mine;
-  if (start < end && at <= start && start < at + mine) {
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long c =
-          (long long)t.Hkv * Split(cached_len(t, b), live_nodes(t, b), a.G).head;
-      if (start < at + c) {
-        scan[12] = b;
-        scan[13] = at;
-        break;
-      }
-      at += c;
-    }
-  }
-  __syncthreads();
+  // Launched as a programmatic dependent of the previous kernel in the
+  // stream: nothing in global memory is touched before it has completed.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // next segment from the ring; every lane of a reading warp takes part
   auto next_seg = [&](int& k, Seg& s) -> bool {
@@ -371,6 +335,48 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     return true;
   };
 
+  // The Q rows of a segment, `part` of `parts` of them, by one warp: row r of the
+  // unit is node r % nb of head r / nb.  A lane copies one 16-byte chunk of
+  // every (32 / chunks)-th row, to each of the row's copies.
+  auto load_q = [&](const Seg& s, int qt, int part, int parts) -> bool {
+    constexpr int kChunks = D / 8, kStep = 32 / kChunks, span = kTile / kCopies;
+    const int c = lane % kChunks, rows = group_rows(s);
+    const int nq = kWide && rows > kTile ? 2 : 1;
+    const int dg = kStep / s.nb, di = kStep % s.nb;
+    const __nv_bfloat16* qb = t.q + ((size_t)s.b * t.Hq + (size_t)s.h * a.G) * t.Nq * D + c * 8;
+    for (int sl = 0; sl < nq; ++sl) {
+      const int buf = (qt + sl) & 1;
+      if (!mbar_wait_warp(&bars[L::Q_EMPTY + buf], (((qt + sl) >> 1) & 1) ^ 1, abort_flag))
+        return false;
+      const uint32_t dst = smem_u32(smem + L::kQ + buf * L::kTileBytes) +
+                           (uint32_t)(c >> 3) * L::kBox;
+      const int r0 = s.rg * 2 * kTile + sl * kTile, some = span / parts;
+      int r_end = rows - sl * kTile < span ? rows - sl * kTile : span;
+      if (r_end > (part + 1) * some) r_end = (part + 1) * some;
+      int r = part * some + lane / kChunks, gh = (r0 + r) / s.nb, i = (r0 + r) % s.nb;
+#pragma unroll 4
+      for (; r < r_end; r += kStep) {
+        const __nv_bfloat16* src = qb + ((size_t)gh * t.Nq + i) * D;
+#pragma unroll
+        for (int cp = 0; cp < kCopies; ++cp)
+          cp_async_16(dst + sw128_offset(r + cp * span, c & 7), src);
+        gh += dg;
+        i += di;
+        if (i >= s.nb) { i -= s.nb; ++gh; }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int sl = 0; sl < nq; ++sl) {   // (the second tile's rows are on their way too)
+      if (sl + 1 < nq) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int x = parts; x < 3; ++x) mbar_arrive(&bars[L::Q_FULL + ((qt + sl) & 1)]);
+    }
+    return true;
+  };
+
   if (warp == 9) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -381,13 +387,41 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     }
     int k = 0, g = 0;        // segments and ring positions so far
     bool ok = true;
-    Record rec;
-    rec.last = -1;
-    rec.T = T;
     int b = 0, h = 0, rg = 0, j0 = 0, Lb = 0, nb = 0;
     long long p0 = 0;        // where the current unit starts
     Split sp(0, 0, 1);
+    // total cost, and the sequence in which this CTA's share starts: a lane
+    // sums `per` sequences, the warp the lanes' sums
+    auto seq_cost = [&](int i) -> long long {
+      return (long long)t.Hkv * Split(cached_len(t, i), live_nodes(t, i), a.G).head;
+    };
+    const int per = (t.B + 31) >> 5;
+    long long mine = 0;
+#pragma unroll 4
+    for (int i = lane * per; i < (lane + 1) * per; ++i)
+      if (i < t.B) mine += seq_cost(i);
+    long long at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    const long long T = __shfl_sync(0xffffffffu, at, 31);
+    at -= mine;
+    const Cuts cuts(T, a);
+    const long long start = cuts.at(blockIdx.x), end = cuts.at(blockIdx.x + 1);
     bool more = start < end;
+    if (more) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, at <= start && start < at + mine)) - 1;
+      b = lane * per;
+      if (lane == src && per > 1)
+        for (long long c; at + (c = seq_cost(b)) <= start; at += c) ++b;
+      b = __shfl_sync(0xffffffffu, b, src);
+      at = __shfl_sync(0xffffffffu, at, src);
+    }
+    Record rec;
+    rec.last = -1;
+    rec.T = T;
     // first unit with live nodes at or after (b, 0, 0)
     auto load_seq = [&]() {
       for (; b < t.B; ++b) {
@@ -410,9 +444,8 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       }
     };
     if (more) {
-      b = (int)scan[12];
       load_seq();
-      long long rel = start - scan[13];
+      long long rel = start - at;
       h = (int)div_pos(rel, sp.head);
       rel -= h * sp.head;
       rg = (int)div_pos(rel, sp.unit(kCostPair));
@@ -593,61 +626,26 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
     // every MMA of this CTA must be complete before TMEM is released
     commit(L::MMA_DONE);
     mbar_wait_warp(&bars[L::MMA_DONE], 0, nullptr);
-  } else if (warp == 11) {
+  } else if (!kWide && warp == 11) {
     // ------------------------------------------------------------ V tiles
     int k = 0, g = 0;
     Seg s;
     while (next_seg(k, s)) {
+      if (k == 1 && !load_q(s, 0, 1, 2)) break;   // half of the first segment's Q
       if (!load_tiles(s, g, true)) break;
       g += 2 * s.n;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 10) {
     // ------------------------------------------------------------ Q rows
-    // Row r of the unit is node r % nb of head r / nb.  A lane copies chunk
-    // `c` of every (32 / chunks)-th row, to each of the row's copies.
-    constexpr int kChunks = D / 8, kStep = 32 / kChunks;
-    const int c = lane % kChunks;
     int k = 0, qt = 0;
-    bool ok = true;
     Seg s;
-    while (ok && next_seg(k, s)) {
-      const int rows = group_rows(s);
-      const int nq = kWide && rows > kTile ? 2 : 1;
-      // (one row tile: all of its 128 lanes hold rows, see the softmax)
-      constexpr int span = kTile / kCopies;
-      const int dg = kStep / s.nb, di = kStep % s.nb;
-      const __nv_bfloat16* qb =
-          t.q + ((size_t)s.b * t.Hq + (size_t)s.h * a.G) * t.Nq * D + c * 8;
-      for (int sl = 0; sl < nq; ++sl) {
-        const int buf = (qt + sl) & 1;
-        if (!mbar_wait_warp(&bars[L::Q_EMPTY + buf], (((qt + sl) >> 1) & 1) ^ 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = smem_u32(smem + L::kQ + buf * L::kTileBytes) +
-                             (uint32_t)(c >> 3) * L::kBox;
-        const int r0 = s.rg * 2 * kTile + sl * kTile;
-        const int r_end = rows - sl * kTile < span ? rows - sl * kTile : span;
-        int r = lane / kChunks, gh = (r0 + r) / s.nb, i = (r0 + r) % s.nb;
-        for (; r < r_end; r += kStep) {
-          const __nv_bfloat16* src = qb + ((size_t)gh * t.Nq + i) * D;
-#pragma unroll
-          for (int cp = 0; cp < kCopies; ++cp)
-            cp_async_16(dst + sw128_offset(r + cp * span, c & 7), src);
-          gh += dg;
-          i += di;
-          if (i >= s.nb) { i -= s.nb; ++gh; }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      }
-      for (int sl = 0; ok && sl < nq; ++sl) {   // (the second tile's rows are on their way too)
-        if (sl + 1 < nq) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::Q_FULL + ((qt + sl) & 1)]);
-      }
-      qt += nq;
+    int g = 0;
+    while (next_seg(k, s)) {
+      if (!load_q(s, qt, 0, !kWide && k == 1 ? 2 : 1)) break;
+      qt += kWide && group_rows(s) > kTile ? 2 : 1;
+      if (kWide && !load_tiles(s, g, true)) break;
+      g += 2 * s.n;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     // rows of the nodes a sequence does not have
@@ -958,10 +956,25 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       const int warp_row = lr - lane;
       const bool idle = warp_row >= rows;                // no live row in this warp
       const bool dead = lr >= rows;                      // computes on anything, is not stored
-      const int rr = s.rg * 2 * kTile + (lr < rows ? lr : rows - 1);
-      const int head = rr / s.nb, node = rr - head * s.nb;
       float m_run = -INFINITY, l_run = 0.f;
       const int steps = pair ? n : (n + 1 - sl) / 2;
+      auto rescale = [&](int x, bool need, float m_tile) {
+        const float m_new = need ? m_tile : m_run;
+        if (x > 0) {
+          const float f = (need && m_run != -INFINITY) ? exp2_approx(m_run - m_new) : 1.f;
+          l_run *= f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tc::ld32f(ocol + 32 * c, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tc::st32f(ocol + 32 * c, o);
+          }
+        }
+        m_run = m_new;
+      };
       for (int x = 0; x < steps; ++x) {
         const int j = pair ? x : 2 * x + sl;
         const int jt = s.j0 + j;                         // tile of the unit
@@ -981,7 +994,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
             // the node and its ancestors among drafts [base, base + 128)
             const int base = (jt - np) * kTile;
             const int32_t* par = t.parents + (size_t)s.b * t.Nq;
-            int v = node;
+            int v = (s.rg * 2 * kTile + (dead ? rows - 1 : lr)) % s.nb;
             while (v >= base) {
               const int e = v - base;
               if (e < kTile) {
@@ -1029,40 +1042,46 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
         // in log2 units), so P is computed with it from a single read of S
         // and kept if no live row of the warp needs a rescale.  (The branch
         // is on what the whole warp shares: tcgen05 moves are warp-wide.)
-        if (!masked && x > 0) {
-          const float2 c_sl2 = make_float2(sl2, sl2), c_m = make_float2(-m_run, -m_run);
+        if (!masked) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t pk[64];
-          float rsum = 0.f;
 #pragma unroll
-          for (int c8 = 0; c8 < 2; ++c8) {
+          for (int c = 0; c < 2; ++c) {
             float sv[64];
-            tc::ld32f(scol + 64 * c8, sv);
-            tc::ld32f(scol + 64 * c8 + 32, sv + 32);
+            tc::ld32f(scol + 64 * c, sv);
+            tc::ld32f(scol + 64 * c + 32, sv + 32);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) m4[e & 3] = max3(m4[e & 3], sv[2 * e], sv[2 * e + 1]);
+          }
+          const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+          const bool need = !dead && m_tile > m_run + kRescaleLog2;
+          if (__any_sync(0xffffffffu, need)) rescale(x, need, m_tile);
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          const float2 c_sl2 = make_float2(sl2, sl2), c_m = make_float2(-mu, -mu);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float sv[64];
+            uint32_t pk[32];
+            tc::ld32f(scol + 64 * c, sv);
+            tc::ld32f(scol + 64 * c + 32, sv + 32);
             tc::wait_ld();
             float2 rs2 = make_float2(0.f, 0.f), rs3 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              m4[e & 3] = max3(m4[e & 3], sv[2 * e], sv[2 * e + 1]);
               const float2 y = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), c_sl2, c_m);
               const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
               if (e & 1) rs3 = __fadd2_rn(rs3, p); else rs2 = __fadd2_rn(rs2, p);
-              pk[32 * c8 + e] = pack_bf16x2(p.x, p.y);
+              pk[e] = pack_bf16x2(p.x, p.y);
             }
             rs2 = __fadd2_rn(rs2, rs3);
-            rsum += rs2.x + rs2.y;
+            l_run += rs2.x + rs2.y;
+            tc::st16(scol + 32 * c, pk);
+            tc::st16(scol + 32 * c + 16, pk + 16);
           }
-          const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
-          const bool keep = m_run != -INFINITY && !(m_tile > m_run + kRescaleLog2);
-          if (__all_sync(0xffffffffu, keep || dead)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc::st16(scol + 16 * c, pk + 16 * c);
-            l_run += rsum;
-            tc::wait_st();
-            tc::fence_before();
-            mbar_arrive(&bars[L::P_FULL + sl]);
-            continue;
-          }
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&bars[L::P_FULL + sl]);
+          continue;
         }
         // two passes over S, in chunks of 32 keys: a chunk that no row of the
         // warp sees is skipped, one that every row sees takes no mask
@@ -1080,23 +1099,7 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
         }
         const float m_tile = mx * sl2;
         const bool need = !dead && m_tile > m_run + kRescaleLog2;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = need ? m_tile : m_run;
-          if (x > 0) {
-            const float f = (need && m_run != -INFINITY) ? exp2_approx(m_run - m_new) : 1.f;
-            l_run *= f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tc::ld32f(ocol + 32 * c, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tc::st32f(ocol + 32 * c, o);
-            }
-          }
-          m_run = m_new;
-        }
+        if (__any_sync(0xffffffffu, need)) rescale(x, need, m_tile);
         const float m_use = m_run == -INFINITY ? 0.f : m_run;
         float rs = 0.f;
 #pragma unroll 1
@@ -1158,8 +1161,9 @@ __global__ void __launch_bounds__(tr::kThreads, 1)
       const bool direct = (s.flags & 2) != 0;
       const int slot = 2 * blockIdx.x + ((s.flags & 1) ? 0 : 1);
       const bool store = !dead;
+      const int rr = s.rg * 2 * kTile + (dead ? rows - 1 : lr), head = rr / s.nb;
       const size_t orow =
-          ((size_t)s.b * t.Hq + (size_t)s.h * a.G + head) * t.Nq + node;
+          ((size_t)s.b * t.Hq + (size_t)s.h * a.G + head) * t.Nq + (rr - head * s.nb);
       const size_t prow = (size_t)slot * a.RP + lr;
       // pair: all columns of the own slot; else half of the columns of both
       const uint32_t oa = tmem + lane_off + 256u + (pair ? (uint32_t)D * sl : 0u);
@@ -1362,7 +1366,7 @@ int launch_tree_k(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& t
   constexpr int smem = tr::Smem<D>::kTotal;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return ATTN_ECUDA;
-  const int rc = launch_programmatic(kern, dim3(a.grid), dim3(tr::kThreads), smem, st, tk, tv, tkn,
+  const int rc = launch_programmatic(kern, dim3(a.grid), dim3(tr::threads(kKeys == 0)), smem, st, tk, tv, tkn,
                                      tvn, a);
   if (rc != ATTN_OK) return rc;
   constexpr int HB = kJoinWarps * kJoinRows;
