@@ -478,6 +478,12 @@ class _On:
             t.record_stream(self.other)
         return t
 
+    def like(self, t):      # of a contiguous tensor
+        t = _torch().empty_like(t)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
 
 def _data(t):
     return None if t is None else t.data_ptr()
@@ -495,13 +501,17 @@ def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N,
     there is none; state_out int32 [2], the queue's new state (a tensor of its
     own: pass it as the next call's state).  Page shortage is reported by
     device_status() (ATTN_ERANGE)."""
-    i32 = _torch().int32
-    _check_tensor(block_table, "block_table", i32, 2)
-    _check_tensor(free_pages, "free_pages", i32, 1)
-    B, max_pages = block_table.shape
-    num_pages = free_pages.numel()
-    args = [(old_lens, "old_lens", i32, (B,)), (new_lens, "new_lens", i32, (B,)),
-            (free_pages, "free_pages", i32, (num_pages,)), (state, "state", i32, (2,))]
+    torch = _torch()
+    i32 = torch.int32
+    try:
+        (B, max_pages), (num_pages,) = block_table.shape, free_pages.shape
+    except (AttributeError, ValueError):
+        _check_tensor(block_table, "block_table", i32, 2)
+        _check_tensor(free_pages, "free_pages", i32, 1)
+        raise
+    args = [(block_table, "block_table", i32, (B, max_pages)), (old_lens, "old_lens", i32, (B,)),
+            (new_lens, "new_lens", i32, (B,)), (free_pages, "free_pages", i32, (num_pages,)),
+            (state, "state", i32, (2,))]
     if index is not None:
         args.append((index, "index", i32, (B, N)))
     if slots is not None:
@@ -512,7 +522,7 @@ def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N,
         if slots is None:
             slots = on.new(block_table, (B, N), i32)
         if state_out is None:
-            state_out = on.new(block_table, (2,), i32)
+            state_out = on.like(state)
         rc = lib().paged_plan(old_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
                               free_pages.data_ptr(), state.data_ptr(), state_out.data_ptr(),
                               _data(index), slots.data_ptr(), B, N, max_pages, int(page_size),
@@ -637,23 +647,28 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
     or beyond new_lens[b] are 0 and -inf."""
     torch = _torch()
     bf, i32 = torch.bfloat16, torch.int32
-    _check_tensor(q, "q", bf, 4)
-    _check_tensor(k_new, "k_new", bf, 4)
-    _check_tensor(k_cache, "k_cache", bf, 4)
-    B, Hq, Nq, d = shape = q.shape
-    Bn, Hkv, Nn, dn = new = k_new.shape
-    cs = k_cache.shape
+    try:
+        B, Hq, Nq, d = shape = q.shape
+        Bn, Hkv, Nn, dn = new = k_new.shape
+        _, _, _, _ = cs = k_cache.shape
+    except (AttributeError, ValueError):
+        for t, n in ((q, "q"), (k_new, "k_new"), (k_cache, "k_cache")):
+            _check_tensor(t, n, bf, 4)
+        raise
     if Bn != B or Nn != Nq or dn != d or v_new.shape != new:
+        for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
+            _check_tensor(t, n, bf, 4)
         raise ValueError(f"shape mismatch q{tuple(shape)} k_new{tuple(new)} "
                          f"v_new{tuple(v_new.shape)}")
     if v_cache.shape != cs or cs[1] != Hkv or cs[3] != d:
         raise ValueError(f"cache shapes {tuple(cs)}, {tuple(v_cache.shape)} do not match "
                          f"k_new{tuple(new)}")
-    args = [(k_cache, "k_cache", bf, cs), (v_cache, "v_cache", bf, cs), (k_new, "k_new", bf, new),
+    args = [(q, "q", bf, shape), (k_cache, "k_cache", bf, cs), (v_cache, "v_cache", bf, cs), (k_new, "k_new", bf, new),
             (v_new, "v_new", bf, new), (parents, "parents", i32, (B, Nq))]
     max_pages = num_pages = page_size = Nk = 0
     if block_table is not None:
-        _check_tensor(block_table, "block_table", i32, 2)
+        if block_table.dim() != 2:
+            _check_tensor(block_table, "block_table", i32, 2)
         rows, max_pages = block_table.shape
         if rows != B:
             raise ValueError(f"block_table has {rows} rows, expected B = {B}")
@@ -666,7 +681,6 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
             raise ValueError(f"cache has {cs[0]} sequences, expected B = {B}")
         Nk = cs[2]
     if key_lens is not None:
-        _check_tensor(key_lens, "key_lens", i32, 1)
         if key_lens.numel() != B:
             raise ValueError(f"key_lens has {key_lens.numel()} entries, expected B = {B}")
         args.append((key_lens, "key_lens", i32, (B,)))
@@ -683,7 +697,7 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
         args.append((workspace, "workspace", torch.uint8, workspace.shape))
     with _On(_check_all(q, args), stream) as on:
         if out is None:
-            out = on.new(q, shape, bf)
+            out = on.like(q)
         if return_lse and lse is None:
             lse = on.new(q, (B, Hq, Nq), torch.float32)
         L = lib()

@@ -67,6 +67,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
   __shared__ long long s_red[4][kPlanThreads / 32];
   __shared__ PlanSeq s_seq[kPlanMaxS];
   __shared__ long long s_take[kPlanMaxS], s_give[kPlanMaxS];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = blockIdx.x / a.chunks, chunk = blockIdx.x - grp * a.chunks;
   const int b0 = grp * a.S;
@@ -187,8 +189,7 @@ int launch_paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t*
   if (a.S > kPlanMaxS) a.S = kPlanMaxS;
   a.chunks = a.S > 1 ? 1 : (N + kPlanItems - 1) / kPlanItems;
   const long long grid = (long long)((B + a.S - 1) / a.S) * a.chunks;
-  paged_plan_kernel<<<(unsigned)grid, kPlanThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ECUDA;
+  return launch_programmatic(paged_plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), 0, st, a);
 }
 
 // ------------------------------------------------------------------ append
@@ -200,10 +201,13 @@ int launch_paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t*
 // a list of the tokens that have a slot, then streams the rows: a thread
 // takes 32 bytes of a row -- the two 16-byte chunks that hold its 8 pairs --
 // and writes them to q_out / k_out and to the cache.  Bound by HBM for
-// prompts, by latency for a decode step.
+// prompts (4 x 8192 tokens of 32 + 8 + 8 heads, 806 MB: 146 us, 5.5 TB/s; with
+// one item of a thread at a time 167, with 3 blocks an SM 211), by latency for
+// a decode step (64 tokens: 4.4 us, 0.8 of them the 64-bit power).
 
 namespace {
 constexpr int kAppThreads = 256;
+constexpr int kBatch = 2;        // items of a thread whose loads are on their way together
 
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -225,30 +229,43 @@ struct AppendArgs {
 };
 
 template <int D, bool kRope, bool kAdjacent, int TT>
-__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(AppendArgs a) {
   constexpr int kHalf = D / 2;
-  constexpr int kChunks = D / 16;     // 32-byte items of a row
-  __shared__ float2 tab[kRope ? TT * kHalf : 1];
-  __shared__ int s_slot[TT], s_list[TT];
+  constexpr int kChunks = D / 16;                  // 32-byte items of a row
+  constexpr int kRows = kAppThreads / kChunks;     // rows that the block takes at once
+  __shared__ __align__(16) float2 tab[kRope ? TT * kHalf : 2];
+  __shared__ long long s_src[3][TT];   // a token's row in q, k, v (elements)
+  __shared__ int s_b[TT], s_i[TT];
+  __shared__ long long s_cache[TT];    // its row in the cache, or -1 (elements)
+  __shared__ int s_list[TT];           // the tokens that are stored
   __shared__ int s_kept;
   const int tid = threadIdx.x;
   const long long T = (long long)a.B * a.N;
   const long long t0 = (long long)blockIdx.x * TT;
   const int nt = T - t0 < TT ? (int)(T - t0) : TT;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid < 32) {
-    // slots of the tile's tokens, and the list of those that are stored
     const long long rows = (long long)a.num_pages * a.page_size;
-    int s = -1;
-    if (a.slots && tid < nt) {
-      s = a.slots[t0 + tid];
-      if (s >= rows) {
-        s = -1;
+    int slot = -1;
+    if (tid < nt) {
+      if (a.slots) slot = a.slots[t0 + tid];
+      const int b = (int)((unsigned)(t0 + tid) / (unsigned)a.N);   // (B * N < 2^31)
+      const int i = (int)(t0 + tid - (long long)b * a.N);
+      s_b[tid] = b;
+      s_i[tid] = i;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) s_src[p][tid] = b * a.sb[p] + i * a.st[p];
+      if (slot >= rows) {
+        slot = -1;
         atomicExch(&g_device_status, (int)ATTN_ERANGE);
       }
+      const int page = slot < 0 ? 0 : slot / a.page_size;
+      s_cache[tid] = slot < 0 ? -1
+                              : ((long long)page * a.Hkv * a.page_size + (slot - page * a.page_size)) * D;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, s >= 0);
-    if (tid < TT) s_slot[tid] = s;
-    if (s >= 0) s_list[__popc(m & ((1u << tid) - 1))] = tid;
+    const unsigned m = __ballot_sync(0xffffffffu, slot >= 0);
+    if (slot >= 0) s_list[__popc(m & ((1u << tid) - 1))] = tid;
     if (tid == 0) s_kept = __popc(m);
   }
   if constexpr (kRope) {
@@ -264,73 +281,91 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(AppendArgs a) {
   const int kept = s_kept;
   const int h0 = (int)((long long)a.heads * blockIdx.y / a.slabs);
   const int h1 = (int)((long long)a.heads * (blockIdx.y + 1) / a.slabs);
+  const int c = tid % kChunks;
 
+#pragma unroll 1
   for (int part = 0; part < 3; ++part) {
     // head rows of this part in the slab
     const int p0 = part == 0 ? 0 : (part == 1 ? a.Hq : a.Hq + a.Hkv);
     const int p1 = part == 0 ? a.Hq : (part == 1 ? a.Hq + a.Hkv : a.heads);
-    const int f = h0 > p0 ? h0 : p0, e = h1 < p1 ? h1 : p1;
-    if (f >= e) continue;
+    const int f = (h0 > p0 ? h0 : p0) - p0, e = (h1 < p1 ? h1 : p1) - p0;
     __nv_bfloat16* out = part == 0 ? a.q_out : (part == 1 ? a.k_out : nullptr);
     __nv_bfloat16* cache = part == 0 ? nullptr : (part == 1 ? a.kc : a.vc);
     const int H = part == 0 ? a.Hq : a.Hkv;
     // without a copy outside the cache only the stored tokens matter
     const int n = out ? nt : kept;
+    if (f >= e || n == 0) continue;
     const bool rot = kRope && part < 2;
     // chunks of an item: pairs (i, i + D/2) sit in chunk c of each half,
     // adjacent pairs and plain copies in two neighbouring chunks
     const bool halves = rot && !kAdjacent;
-    for (int it = tid; it < (e - f) * n * kChunks; it += kAppThreads) {
-      const int c = it % kChunks;
-      const int r = it / kChunks;
-      const int li = r % n;
-      const int h = f - p0 + r / n;
-      const int t = out ? li : s_list[li];
-      const long long tok = t0 + t;
-      const int b = (int)(tok / a.N), i = (int)(tok - (long long)b * a.N);
-      const int e0 = halves ? 8 * c : 16 * c, e1 = halves ? kHalf + 8 * c : 16 * c + 8;
-      const __nv_bfloat16* src =
-          a.x[part] + b * a.sb[part] + h * a.sh[part] + i * a.st[part];
-      uint4 va = *reinterpret_cast<const uint4*>(src + e0);
-      uint4 vb = *reinterpret_cast<const uint4*>(src + e1);
-      if (rot) {
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-        uint32_t oa[4], ob[4];
-        const float2* cs = tab + t * kHalf + 8 * c;
-        if constexpr (kAdjacent) {
+    const int e0 = halves ? 8 * c : 16 * c, e1 = halves ? kHalf + 8 * c : 16 * c + 8;
+    const __nv_bfloat16* x = a.x[part];
+    const long long sh = a.sh[part];
+    // rows (head, token) side by side; a thread steps kRows rows on
+    const int dh = kRows / n, dl = kRows % n;
+    int h = f + (tid / kChunks) / n, li = (tid / kChunks) % n;
+    // several items at a time, their loads first: outputs may be the inputs
+    // themselves, so no load can be moved above an earlier item's stores
+    while (h < e) {
+      uint4 va[kBatch], vb[kBatch];
+      int ts[kBatch], hs[kBatch];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float r0, r1;
-            rope_rotate(lo_bf16(wa[k]), hi_bf16(wa[k]), cs[k], r0, r1);
-            oa[k] = pack_bf16x2(r0, r1);
-            rope_rotate(lo_bf16(wb[k]), hi_bf16(wb[k]), cs[4 + k], r0, r1);
-            ob[k] = pack_bf16x2(r0, r1);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float ra0, rb0, ra1, rb1;
-            rope_rotate(lo_bf16(wa[k]), lo_bf16(wb[k]), cs[2 * k], ra0, rb0);
-            rope_rotate(hi_bf16(wa[k]), hi_bf16(wb[k]), cs[2 * k + 1], ra1, rb1);
-            oa[k] = pack_bf16x2(ra0, ra1);
-            ob[k] = pack_bf16x2(rb0, rb1);
-          }
+      for (int u = 0; u < kBatch; ++u) {
+        hs[u] = h;
+        ts[u] = 0;
+        if (h < e) {
+          ts[u] = out ? li : s_list[li];
+          const __nv_bfloat16* src = x + s_src[part][ts[u]] + h * sh;
+          va[u] = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+          vb[u] = __ldcs(reinterpret_cast<const uint4*>(src + e1));
         }
-        va = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-        vb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        h += dh;
+        li += dl;
+        if (li >= n) { li -= n; ++h; }
       }
-      if (out) {
-        __nv_bfloat16* o = out + (((size_t)b * H + h) * a.N + i) * D;
-        *reinterpret_cast<uint4*>(o + e0) = va;
-        *reinterpret_cast<uint4*>(o + e1) = vb;
-      }
-      const int slot = s_slot[t];
-      if (cache && slot >= 0) {
-        const int page = slot / a.page_size;
-        __nv_bfloat16* o =
-            cache + (((size_t)page * a.Hkv + h) * a.page_size + (slot - page * a.page_size)) * D;
-        *reinterpret_cast<uint4*>(o + e0) = va;
-        *reinterpret_cast<uint4*>(o + e1) = vb;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (hs[u] >= e) break;
+        const int t = ts[u];
+        if (rot) {
+          const uint32_t wa[4] = {va[u].x, va[u].y, va[u].z, va[u].w};
+          const uint32_t wb[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+          uint32_t oa[4], ob[4];
+          const float4* cs = reinterpret_cast<const float4*>(tab + t * kHalf + 8 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kAdjacent) {
+              const float4 p = cs[k >> 1], w = cs[2 + (k >> 1)];
+              const float2 cp = (k & 1) ? make_float2(p.z, p.w) : make_float2(p.x, p.y);
+              const float2 cw = (k & 1) ? make_float2(w.z, w.w) : make_float2(w.x, w.y);
+              float r0, r1;
+              rope_rotate(lo_bf16(wa[k]), hi_bf16(wa[k]), cp, r0, r1);
+              oa[k] = pack_bf16x2(r0, r1);
+              rope_rotate(lo_bf16(wb[k]), hi_bf16(wb[k]), cw, r0, r1);
+              ob[k] = pack_bf16x2(r0, r1);
+            } else {
+              const float4 p = cs[k];
+              float ra0, rb0, ra1, rb1;
+              rope_rotate(lo_bf16(wa[k]), lo_bf16(wb[k]), make_float2(p.x, p.y), ra0, rb0);
+              rope_rotate(hi_bf16(wa[k]), hi_bf16(wb[k]), make_float2(p.z, p.w), ra1, rb1);
+              oa[k] = pack_bf16x2(ra0, ra1);
+              ob[k] = pack_bf16x2(rb0, rb1);
+            }
+          }
+          va[u] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+          vb[u] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+        if (out) {
+          __nv_bfloat16* o = out + (((size_t)s_b[t] * H + hs[u]) * a.N + s_i[t]) * D;
+          *reinterpret_cast<uint4*>(o + e0) = va[u];
+          *reinterpret_cast<uint4*>(o + e1) = vb[u];
+        }
+        if (cache && s_cache[t] >= 0) {
+          __nv_bfloat16* o = cache + s_cache[t] + (size_t)hs[u] * a.page_size * D;
+          *reinterpret_cast<uint4*>(o + e0) = va[u];
+          *reinterpret_cast<uint4*>(o + e1) = vb[u];
+        }
       }
     }
   }
@@ -340,17 +375,19 @@ namespace {
 template <int D, bool kRope, bool kAdjacent>
 int launch_append_t(AppendArgs a, cudaStream_t st) {
   const long long T = (long long)a.B * a.N;
-  // a tile of 32 tokens fills the machine from some 10k tokens on; below
-  // that smaller tiles and slabs of heads spread the rows over the SMs
+  // a tile of 16 tokens fills the machine from some 5k tokens on (8, 24 and 32
+  // took 1 to 6% longer on 32k); below that smaller tiles and slabs of heads
+  // spread the rows over the SMs
   const bool small = T <= 1024;
-  const long long tiles = (T + (small ? 4 : 32) - 1) / (small ? 4 : 32);
+  const long long tiles = (T + (small ? 4 : 16) - 1) / (small ? 4 : 16);
   long long slabs = (296 + tiles - 1) / tiles;
   if (slabs > a.heads) slabs = a.heads;
   a.slabs = (int)slabs;
   const dim3 grid((unsigned)tiles, (unsigned)slabs);
-  if (small) kv_append_kernel<D, kRope, kAdjacent, 4><<<grid, kAppThreads, 0, st>>>(a);
-  else kv_append_kernel<D, kRope, kAdjacent, 32><<<grid, kAppThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ECUDA;
+  return small ? launch_programmatic(kv_append_kernel<D, kRope, kAdjacent, 4>, grid,
+                                     dim3(kAppThreads), 0, st, a)
+               : launch_programmatic(kv_append_kernel<D, kRope, kAdjacent, 16>, grid,
+                                     dim3(kAppThreads), 0, st, a);
 }
 }  // namespace
 
