@@ -417,32 +417,25 @@ def rope_apply(x, base=10000.0, pos_offset=0, pairing=0, out=None, stream=None):
 
 
 # The serving calls run once per step or per layer, often on small tensors,
-# where the host is what they cost: an argument's type, shape, device and
-# layout are looked at once, and the reason is looked for only when one of
-# them does not fit.
+# where the host is what they cost: they look once at each argument's type,
+# device, layout and shape, and for the reason only when one does not fit.
 
-def _check_all(ref, args):
-    """Every (tensor, name, dtype, shape) of `args` has that dtype and shape,
-    is contiguous and on ref's device, a CUDA device, whose index is returned.
-    What is wrong is raised in the library's order: shapes and types of all
-    arguments before devices."""
-    dev = -1
-    try:
-        dev = ref.get_device()
-        for t, _, dtype, shape in args:
-            if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-                    and t.is_contiguous()):
-                dev = -1
-                break
-    except AttributeError:
-        dev = -1
-    if dev < 0:
-        for t, name, dtype, shape in args:
-            _check_tensor(t, name, dtype)
-            if tuple(t.shape) != tuple(shape):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        _check_devices(ref, [(t, name) for t, name, _, _ in args])
-    return dev
+def _same(dev, dtype, *tensors):
+    """Whether these are contiguous tensors of dtype on CUDA device `dev`."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return dev >= 0
+
+
+def _refuse(ref, args):
+    """Raise what is wrong with one of `args` ((tensor, name, dtype, shape)):
+    shapes and types of all of them before devices (ref's)."""
+    for t, name, dtype, shape in args:
+        _check_tensor(t, name, dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _check_devices(ref, [(t, name) for t, name, _, _ in args])
 
 
 class _On:
@@ -509,16 +502,22 @@ def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N,
         _check_tensor(block_table, "block_table", i32, 2)
         _check_tensor(free_pages, "free_pages", i32, 1)
         raise
-    args = [(block_table, "block_table", i32, (B, max_pages)), (old_lens, "old_lens", i32, (B,)),
-            (new_lens, "new_lens", i32, (B,)), (free_pages, "free_pages", i32, (num_pages,)),
-            (state, "state", i32, (2,))]
-    if index is not None:
-        args.append((index, "index", i32, (B, N)))
-    if slots is not None:
-        args.append((slots, "slots", i32, (B, N)))
-    if state_out is not None:
-        args.append((state_out, "state_out", i32, (2,)))
-    with _On(_check_all(block_table, args), stream) as on:
+    args = [(index, "index", i32, (B, N)), (slots, "slots", i32, (B, N)),
+            (state_out, "state_out", i32, (2,))]
+    args = [x for x in args if x[0] is not None]
+    dev = block_table.get_device()
+    try:
+        ok = (old_lens.shape == new_lens.shape == (B,) and state.shape == (2,)
+              and _same(dev, i32, block_table, old_lens, new_lens, free_pages, state)
+              and all(t.shape == shape and _same(dev, i32, t) for t, _, _, shape in args))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(block_table, [(block_table, "block_table", i32, (B, max_pages)),
+                              (old_lens, "old_lens", i32, (B,)), (new_lens, "new_lens", i32, (B,)),
+                              (free_pages, "free_pages", i32, (num_pages,)),
+                              (state, "state", i32, (2,))] + args)
+    with _On(dev, stream) as on:
         if slots is None:
             slots = on.new(block_table, (B, N), i32)
         if state_out is None:
@@ -604,7 +603,13 @@ def kv_append(k, v=None, slots=None, k_cache=None, v_cache=None, q=None, positio
         args.append((q_out, "q_out", bf, q.shape))
     if k_out is not None:
         args.append((k_out, "k_out", bf, shape))
-    dev = _check_all(k, args)
+    dev = k.get_device()
+    try:
+        ok = dev >= 0 and all(t.shape == sh and _same(dev, dt, t) for t, _, dt, sh in args)
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(k, args)
     for t, n in rows:
         if t.get_device() != dev:
             _check_devices(k, [(t, n)])
@@ -627,6 +632,9 @@ def kv_append(k, v=None, slots=None, k_cache=None, v_cache=None, q=None, positio
 
 
 _Strides9 = ctypes.c_int64 * 9
+
+
+_tree_ws_bytes = {}   # of sizes seen: (device, sizes) -> bytes
 
 
 def attn_tree_workspace_size(B, Hq, Hkv, Nq, d) -> int:
@@ -655,6 +663,9 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
         for t, n in ((q, "q"), (k_new, "k_new"), (k_cache, "k_cache")):
             _check_tensor(t, n, bf, 4)
         raise
+    for t, n in ((v_new, "v_new"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
     if Bn != B or Nn != Nq or dn != d or v_new.shape != new:
         for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
             _check_tensor(t, n, bf, 4)
@@ -663,24 +674,25 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
     if v_cache.shape != cs or cs[1] != Hkv or cs[3] != d:
         raise ValueError(f"cache shapes {tuple(cs)}, {tuple(v_cache.shape)} do not match "
                          f"k_new{tuple(new)}")
-    args = [(q, "q", bf, shape), (k_cache, "k_cache", bf, cs), (v_cache, "v_cache", bf, cs), (k_new, "k_new", bf, new),
-            (v_new, "v_new", bf, new), (parents, "parents", i32, (B, Nq))]
+    args = []
     max_pages = num_pages = page_size = Nk = 0
     if block_table is not None:
-        if block_table.dim() != 2:
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
             _check_tensor(block_table, "block_table", i32, 2)
         rows, max_pages = block_table.shape
         if rows != B:
             raise ValueError(f"block_table has {rows} rows, expected B = {B}")
         if key_lens is None:
             raise ValueError("attn_fwd_tree over a paged cache needs key_lens")
-        args.append((block_table, "block_table", i32, (B, max_pages)))
+        args.append((block_table, "block_table", i32, block_table.shape))
         num_pages, page_size = cs[0], cs[2]
     else:
         if cs[0] != B:
             raise ValueError(f"cache has {cs[0]} sequences, expected B = {B}")
         Nk = cs[2]
     if key_lens is not None:
+        if not isinstance(key_lens, torch.Tensor) or key_lens.dim() != 1:
+            _check_tensor(key_lens, "key_lens", i32, 1)
         if key_lens.numel() != B:
             raise ValueError(f"key_lens has {key_lens.numel()} entries, expected B = {B}")
         args.append((key_lens, "key_lens", i32, (B,)))
@@ -695,14 +707,28 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
     if workspace is not None:
         _check_workspace(workspace)
         args.append((workspace, "workspace", torch.uint8, workspace.shape))
-    with _On(_check_all(q, args), stream) as on:
+    dev = q.get_device()
+    try:
+        ok = (_same(dev, bf, q, k_cache, v_cache, k_new, v_new) and parents.shape == (B, Nq)
+              and _same(dev, i32, parents)
+              and all(t.shape == sh and _same(dev, dt, t) for t, _, dt, sh in args))
+    except AttributeError:   # not a tensor
+        ok = False
+    if not ok:
+        _refuse(q, [(q, "q", bf, shape), (k_cache, "k_cache", bf, cs), (v_cache, "v_cache", bf, cs),
+                    (k_new, "k_new", bf, new), (v_new, "v_new", bf, new),
+                    (parents, "parents", i32, (B, Nq))] + args)
+    with _On(dev, stream) as on:
         if out is None:
             out = on.like(q)
         if return_lse and lse is None:
             lse = on.new(q, (B, Hq, Nq), torch.float32)
         L = lib()
         if workspace is None:
-            ws_bytes = L.attn_tree_workspace_size(B, Hq, Hkv, Nq, d)
+            key = (dev, Hq, Hkv, Nq, d, B)
+            ws_bytes = _tree_ws_bytes.get(key)
+            if ws_bytes is None:
+                ws_bytes = _tree_ws_bytes[key] = L.attn_tree_workspace_size(B, Hq, Hkv, Nq, d)
             workspace = on.new(q, (max(ws_bytes, 256),), torch.uint8)
         else:
             ws_bytes = workspace.numel()

@@ -520,8 +520,9 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(Combine
   const size_t row0 = ((size_t)b * a.Hq + (size_t)h * a.G) * a.Nq + g0;
   __nv_bfloat16* orow = a.o + row0 * D;
   if (len == 0) {
-    // o / lse may be read by earlier work in the stream only through the split
-    // kernel's inputs, so writing before the dependency wait is safe
+    // wait here as well: a grid that ends without waiting would tell its own
+    // programmatic dependents that all work before it has completed
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int idx = threadIdx.x; idx < gn * D; idx += blockDim.x) orow[idx] = __float2bfloat16(0.f);
     if (a.lse && threadIdx.x < gn) a.lse[row0 + threadIdx.x] = -INFINITY;
     return;

@@ -181,6 +181,14 @@ struct Cuts {
   }
 };
 
+// Eight consecutive TMEM columns (see tc::st16).
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // 4D tiled load (no multicast): one page of a paged cache, d = 128.
 __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int w,
                                             uint64_t* bar) {
@@ -829,7 +837,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
             uint32_t x[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) x[e] = c == copy ? pk[e] : 0u;
-            if constexpr (W == 16) tc::st16(pc + 16 * c, x); else tc::st8(pc + 8 * c, x);
+            if constexpr (W == 16) tc::st16(pc + 16 * c, x); else st8(pc + 8 * c, x);
           }
         }
         tc::wait_st();

@@ -299,6 +299,118 @@ def test_tree_graphs_share_a_workspace(torch, eb):
             d[0].copy_(x["q"])
 
 
+@pytest.mark.parametrize("case", [
+    # B, Hq, Hkv, Nq, d, page size, cached lengths, nodes
+    (2, 64, 1, 40, 64, 16, [300, 1000], [40, 33]),                       # 2560 rows: ten row groups
+    (1, 1, 1, 1024, 64, 0, [100], [1024]),                               # the largest tree
+    (2048, 1, 1, 2, 64, 8, [(i * 7) % 40 for i in range(2048)], [i % 3 for i in range(2048)]),
+], ids=["rows", "nodes", "sequences"])
+def test_tree_largest_counts(torch, eb, case):
+    x = make(torch, *case, seed=17, kind="chain" if case[3] == 1024 else "random")
+    o, lse = call(torch, eb, x)
+    assert eb.device_status() == 0
+    check(torch, o, lse, want(x))
+
+
+@pytest.mark.parametrize("Hq", [4, 64])
+def test_tree_output_on_a_16_byte_boundary(torch, eb, Hq):
+    x = make(torch, 2, Hq, 4, 9, 128, 16, [90, 33], [9, 4], seed=18)
+    n = x["q"].numel()
+    out = torch.empty(n + 8, dtype=torch.bfloat16, device="cuda")[8:].view(x["q"].shape)
+    assert out.data_ptr() % 32 == 16
+    o, lse = call(torch, eb, x, out=out)
+    check(torch, o, lse, want(x))
+
+
+def test_tree_pages_past_4_gib(torch, eb):
+    """Pages at the end of a 5 GiB pool."""
+    Hkv, ps, d, pages = 8, 128, 128, 20480
+    x = make(torch, 2, 8, Hkv, 3, d, ps, [300, 129], [3, 2], seed=19)
+    kc = torch.empty(pages, Hkv, ps, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    table = x["table"].copy()
+    for i, (b, j) in enumerate((b, j) for b in range(2) for j in range(table.shape[1]) if table[b, j] >= 0):
+        p = pages - 1 - i
+        kc[p], vc[p] = x["kc"][int(table[b, j])].cuda(), x["vc"][int(table[b, j])].cuda()
+        x["table"][b, j] = p
+    w = want(x)
+    x["kc"], x["vc"] = kc, vc
+    o, lse = call(torch, eb, x)
+    assert eb.device_status() == 0
+    check(torch, o, lse, w)
+
+
+def test_tree_calls_on_two_streams(torch, eb):
+    """Calls that overlap, each with a workspace of its own."""
+    xs = [make(torch, 3, 8, 4, 16, 128, 16, [2000, 900, 1500], [16, 9, 12], seed=20),
+          make(torch, 2, 16, 16, 25, 64, 0, [1800, 700], [25, 20], seed=21)]
+    ws = [want(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    args = []
+    for x in xs:
+        d = [x["q"].cuda(), x["kc"].cuda(), x["vc"].cuda(), i32(torch, x["L"]), x["kn"].cuda(),
+             x["vn"].cuda(), i32(torch, x["parents"])]
+        args.append((d, dict(new_lens=i32(torch, x["n"]),
+                             block_table=None if x["table"] is None else i32(torch, x["table"]))))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for s, (d, kw) in zip(streams, args):
+            outs.append(eb.attn_fwd_tree(*d, stream=s, **kw))
+    torch.cuda.synchronize()
+    assert eb.device_status() == 0
+    for i, (o, lse) in enumerate(outs):
+        check(torch, o, lse, ws[i % 2])
+
+
+def test_steps_without_synchronising(torch, eb):
+    """Forty steps of plan, append, tree attention and paged decode queued one
+    behind the other give the bits of the same steps with a synchronisation
+    after every call.  (The kernels start before their predecessors end; each
+    one waits for all work before it.)  One sequence stays empty."""
+    B, Hq, Hkv, N, d, ps, mp, pages = 3, 8, 2, 4, 128, 16, 20, 64
+
+    def go(sync):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(5)
+        table = torch.full((B, mp), -1, dtype=torch.int32, device="cuda")
+        ring = torch.arange(pages, dtype=torch.int32, device="cuda")
+        state = torch.tensor([0, pages], dtype=torch.int32, device="cuda")
+        kc = torch.zeros(pages, Hkv, ps, d, dtype=torch.bfloat16, device="cuda")
+        vc = torch.zeros_like(kc)
+        old = torch.zeros(B, dtype=torch.int32, device="cuda")
+        par = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+        grow = torch.tensor([3, 0, 4], dtype=torch.int32, device="cuda")
+        n = torch.tensor([4, 0, 4], dtype=torch.int32, device="cuda")
+        outs = []
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        for _ in range(40):
+            x = torch.randn(B, N, Hq + 2 * Hkv, d, generator=g, device="cuda").bfloat16().transpose(1, 2)
+            pos = old[:, None] + torch.arange(N, dtype=torch.int32, device="cuda")
+            wait()
+            q, k = eb.kv_append(x[:, Hq:Hq + Hkv], q=x[:, :Hq], positions=pos)
+            wait()
+            v = x[:, Hq + Hkv:].contiguous()
+            o, lse = eb.attn_fwd_tree(q, kc, vc, old, k, v, par, new_lens=n, block_table=table)
+            wait()
+            new = old + grow
+            slots, state = eb.paged_plan(old, new, table, ring, state, ps, N)
+            wait()
+            eb.kv_append(k, v, slots, kc, vc)
+            wait()
+            empty = eb.attn_fwd_paged(q[:, :, :1].contiguous(), kc, vc, table, old * 0)[0]
+            wait()
+            o2, lse2 = eb.attn_fwd_paged(q[:, :, :1].contiguous(), kc, vc, table, new)
+            outs += [o, lse, empty, o2, lse2]
+            old = new
+        torch.cuda.synchronize()
+        assert eb.device_status() == 0
+        return outs + [kc, vc, table, state]
+
+    for a, b in zip(go(False), go(True)):
+        assert torch.equal(a, b)
+
+
 def test_verify_step(torch, eb):
     """Plan, append, tree attention and the paged decode together, as a server
     runs them: a prompt, then steps that draft a tree, verify it and store the

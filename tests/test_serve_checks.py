@@ -203,3 +203,26 @@ def test_attn_fwd_tree_binding():
             eb.attn_fwd_tree(*args, **kw)
     with pytest.raises(TypeError):
         eb.attn_fwd_tree(q, c, c, kl, kn, kn, par.long())
+
+
+def test_arguments_that_are_not_tensors():
+    good = [i32(3), i32(3), i32(3, 4), i32(10), i32(2)]
+    for k in range(5):
+        x = list(good)
+        x[k] = [1, 2, 3]
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            eb.paged_plan(*x, 16, 5)
+    k, c, s = bf16(2, 2, 5, 64), bf16(7, 2, 16, 64), i32(2, 5)
+    for args in [(1, k, s, c, c), (k, 1, s, c, c), (k, k, [1], c, c), (k, k, s, 1, c), (k, k, s, c, 1)]:
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            eb.kv_append(*args)
+    q, kn, c, par, kl = bf16(2, 4, 5, 64), bf16(2, 2, 5, 64), bf16(2, 2, 30, 64), i32(2, 5), i32(2)
+    good = [q, c, c, kl, kn, kn, par]
+    for k in range(7):
+        x = list(good)
+        x[k] = [1, 2]
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            eb.attn_fwd_tree(*x)
+    for kw in (dict(block_table=3), dict(new_lens=3), dict(out=3), dict(lse=3), dict(workspace=3)):
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            eb.attn_fwd_tree(*good, **kw)
