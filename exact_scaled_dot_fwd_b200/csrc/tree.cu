@@ -65,9 +65,12 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
              : a / b;
 }
 
-// Costs of the work split, in parts of a tile's HBM time: a tile of up to 128
-// rows, one of a pair, and what a unit's start costs.
-constexpr int kCostTile = 5, kCostPair = 8, kCostUnit = 5;
+// Costs of the work split, in fifths of a tile's HBM time: a tile of up to 128
+// rows, one of a pair, and what one more unit costs a CTA (its epilogue, the
+// next unit's first tiles): measured as the time by which CTAs with two
+// segments end later than those with one, 3.5 to 4.6 us up to 64 rows, 9 above.
+constexpr int kCostTile = 5, kCostPair = 8;
+__host__ __device__ constexpr int unit_cost(int rp) { return rp > 128 ? 32 : (rp > 64 ? 28 : 16); }
 
 template <int D>
 struct Smem {
@@ -106,6 +109,7 @@ struct Args {
   float* part_lse;    // [2 * ranges][RP], log2 units
   struct Record* records;   // [ranges]
   int G, RP, grid, ranges, oob_row;
+  int cost_unit;
 };
 
 // What a range leaves for the join: the unit it starts and does not finish.
@@ -140,9 +144,10 @@ __device__ __forceinline__ int live_nodes(const TreeArgs& t, int b) {
 struct Split {
   int nt;              // tiles of a unit (0: no live node, no unit)
   int nrg;             // row groups of a kv head
+  int cu;              // what a unit costs beside its tiles
   int w_last;          // tile cost of the last row group (the others are pairs)
   long long head;      // cost of a kv head
-  __device__ __forceinline__ Split(int L, int nb, int G) {
+  __device__ __forceinline__ Split(int L, int nb, int G, int cost_unit) : cu(cost_unit) {
     const int rows = G * nb;
     nt = nb > 0 ? (L + kTile - 1) / kTile + (nb + kTile - 1) / kTile : 0;
     nrg = (rows + 2 * kTile - 1) / (2 * kTile);
@@ -150,17 +155,17 @@ struct Split {
     head = nb > 0 ? (long long)(nrg - 1) * unit(kCostPair) + unit(w_last) : 0;
   }
   __device__ __forceinline__ int weight(int rg) const { return rg < nrg - 1 ? kCostPair : w_last; }
-  __device__ __forceinline__ long long unit(int w) const { return kCostUnit + (long long)nt * w; }
+  __device__ __forceinline__ long long unit(int w) const { return cu + (long long)nt * w; }
 };
 
 // Where tile j of a unit starts (the unit's own cost belongs to tile 0), and how
 // many of its nt tiles start before x.
-__device__ __forceinline__ long long tile_at(int j, int w) {
-  return j == 0 ? 0 : kCostUnit + (long long)j * w;
+__device__ __forceinline__ long long tile_at(int j, int w, int cu) {
+  return j == 0 ? 0 : cu + (long long)j * w;
 }
-__device__ __forceinline__ int tiles_before(long long x, int w, int nt) {
+__device__ __forceinline__ int tiles_before(long long x, int w, int nt, int cu) {
   if (x <= 0) return 0;
-  x -= kCostUnit;
+  x -= cu;
   if (x <= 0) return 1;
   const long long j = div_pos(x + w - 1, w);
   return j > nt ? nt : (int)j;
@@ -207,6 +212,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// Node and ancestors of up to 32 nodes as bits, lane i holding the parent of node
+// i (-1: none): each round takes in the set of the ancestor reached so far and
+// doubles the distance to it.  A parent that does not come before its node is
+// reported and taken as none.
+__device__ __forceinline__ uint32_t ancestors32(int parent, int lane) {
+  if (parent < -1 || parent >= lane) {
+    atomicExch(&g_device_status, (int)ATTN_ERANGE);
+    parent = -1;
+  }
+  uint32_t set = 1u << lane;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int from = parent < 0 ? lane : parent;
+    set |= __shfl_sync(0xffffffffu, set, from);
+    const int up = __shfl_sync(0xffffffffu, parent, from);
+    parent = parent < 0 ? -1 : up;
+  }
+  return set;
 }
 
 }  // namespace tr
@@ -397,11 +422,11 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
     bool ok = true;
     int b = 0, h = 0, rg = 0, j0 = 0, Lb = 0, nb = 0;
     long long p0 = 0;        // where the current unit starts
-    Split sp(0, 0, 1);
+    Split sp(0, 0, 1, a.cost_unit);
     // total cost, and the sequence in which this CTA's share starts: a lane
     // sums `per` sequences, the warp the lanes' sums
     auto seq_cost = [&](int i) -> long long {
-      return (long long)t.Hkv * Split(cached_len(t, i), live_nodes(t, i), a.G).head;
+      return (long long)t.Hkv * Split(cached_len(t, i), live_nodes(t, i), a.G, a.cost_unit).head;
     };
     const int per = (t.B + 31) >> 5;
     long long mine = 0;
@@ -430,12 +455,19 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
     Record rec;
     rec.last = -1;
     rec.T = T;
+    int ahead = -1, ahead_L = 0, ahead_n = 0;
     // first unit with live nodes at or after (b, 0, 0)
     auto load_seq = [&]() {
       for (; b < t.B; ++b) {
-        Lb = cached_len(t, b);
-        nb = live_nodes(t, b);
-        sp = Split(Lb, nb, a.G);
+        Lb = b == ahead ? clamp_len(ahead_L, t.Nk) : cached_len(t, b);
+        nb = b == ahead ? clamp_len(ahead_n, t.Nq) : live_nodes(t, b);
+        sp = Split(Lb, nb, a.G, a.cost_unit);
+        // the next sequence's lengths, asked for now and looked at when it comes
+        ahead = b + 1;
+        if (ahead < t.B) {
+          ahead_L = t.key_lens ? t.key_lens[ahead] : t.Nk;
+          ahead_n = t.new_lens ? t.new_lens[ahead] : t.Nq;
+        }
         if (sp.nt > 0) return;
       }
     };
@@ -460,13 +492,13 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       if (rg > sp.nrg - 1) rg = sp.nrg - 1;
       rel -= rg * sp.unit(kCostPair);
       p0 = start - rel;
-      j0 = rel == 0 ? 0 : tiles_before(rel, sp.weight(rg), sp.nt);
+      j0 = rel == 0 ? 0 : tiles_before(rel, sp.weight(rg), sp.nt, a.cost_unit);
       if (j0 == sp.nt) next_unit();
     }
     while (ok) {
       const int w = sp.weight(rg);
       int n = 0;
-      if (more && b < t.B && p0 + tile_at(j0, w) < end) n = tiles_before(end - p0, w, sp.nt) - j0;
+      if (more && b < t.B && p0 + tile_at(j0, w, a.cost_unit) < end) n = tiles_before(end - p0, w, sp.nt, a.cost_unit) - j0;
       const int slot = k % kSegSlots;
       if (!mbar_wait_warp(&bars[L::SEG_EMPTY + slot], ((k / kSegSlots) & 1) ^ 1, abort_flag)) break;
       const bool whole = j0 == 0 && n == sp.nt;
@@ -479,7 +511,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       if (n == 0) break;
       if (j0 == 0 && n < sp.nt) {   // this CTA starts a unit that others finish
         const int rows = a.G * nb - rg * 2 * kTile;
-        rec.last = cuts.of(p0 + tile_at(sp.nt - 1, w));
+        rec.last = cuts.of(p0 + tile_at(sp.nt - 1, w, a.cost_unit));
         rec.slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
         rec.b = b; rec.h = h; rec.rg = rg;
         rec.rows = rows < 2 * kTile ? rows : 2 * kTile;
@@ -696,6 +728,10 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       const int rr = lr < rows ? lr : rows - 1;
       const int head = rr / s.nb, node = rr - head * s.nb;
       float m_run = -INFINITY, l_run = 0.f;
+      // a small tree's parents, asked for here and looked at on its tile
+      const bool small = s.nb <= 32;
+      int parent = -1;
+      if (small && s.j0 + n > np && lane < s.nb) parent = t.parents[(size_t)s.b * t.Nq + lane];
 
       // one tile, NC keys of this thread from key k0 of the tile on
       auto tile = [&](auto mask, int j, int jt, int valid) {
@@ -709,6 +745,9 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
           if (jt < np) {
             const int e = valid - k0;
             seen = e >= 64 ? ~0ull : (e <= 0 ? 0ull : (1ull << e) - 1ull);
+          } else if (small) {
+            const uint32_t set = __shfl_sync(0xffffffffu, ancestors32(parent, lane), node);
+            seen = k0 < 32 ? set >> k0 : 0u;
           } else {
             // the node and its ancestors among drafts [first, first + NC)
             const int first = (jt - np) * kTile + k0;
@@ -965,6 +1004,10 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       const bool idle = warp_row >= rows;                // no live row in this warp
       const bool dead = lr >= rows;                      // computes on anything, is not stored
       float m_run = -INFINITY, l_run = 0.f;
+      // a small tree's parents, asked for here and looked at on its tile
+      const bool small = s.nb <= 32;
+      int parent = -1;
+      if (small && s.j0 + n > np && lane < s.nb) parent = t.parents[(size_t)s.b * t.Nq + lane];
       const int steps = pair ? n : (n + 1 - sl) / 2;
       auto rescale = [&](int x, bool need, float m_tile) {
         const float m_new = need ? m_tile : m_run;
@@ -998,6 +1041,9 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
               const int e = valid - 32 * c;
               bits[c] = e >= 32 ? 0xffffffffu : (e <= 0 ? 0u : (1u << e) - 1u);
             }
+          } else if (small) {
+            const int node = (s.rg * 2 * kTile + (dead ? rows - 1 : lr)) % s.nb;
+            bits[0] = __shfl_sync(0xffffffffu, ancestors32(parent, lane), node);
           } else {
             // the node and its ancestors among drafts [base, base + 128)
             const int base = (jt - np) * kTile;
@@ -1279,7 +1325,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(tr::Args 
     const int c = base + lane;
     bool has = c <= u.last;
     if (has && c > c0)
-      has = tiles_before(cuts.at(c + 1) - u.p0, u.w, u.nt) > tiles_before(cuts.at(c) - u.p0, u.w, u.nt);
+      has = tiles_before(cuts.at(c + 1) - u.p0, u.w, u.nt, a.cost_unit) > tiles_before(cuts.at(c) - u.p0, u.w, u.nt, a.cost_unit);
     unsigned bal = __ballot_sync(0xffffffffu, has);
     while (bal) {
       const int n = __popc(bal) < kJoinParts ? __popc(bal) : kJoinParts;
@@ -1415,6 +1461,7 @@ int launch_tree(const TreeArgs& t, int d, void* workspace, int num_sms, cudaStre
   w += round256(slots * a.RP * sizeof(float));
   a.records = reinterpret_cast<tr::Record*>(w);
   a.ranges = num_sms;
+  a.cost_unit = tr::unit_cost(a.RP);
   // the drafts [B * Hkv, Nq, d] and a contiguous cache [B * Hkv, Nk, d] in
   // boxes of 128 rows x 64 columns; a paged cache page by page
   CUtensorMap tk, tv, tkn, tvn;
