@@ -15,23 +15,33 @@
 // its log-sum-exp per CTA (at most two a CTA, its first and last segment),
 // and a second kernel joins them.
 //
-// Warp roles (12 warps):
-//   0-3, 4-7   softmax of slot 0 and of slot 1 (a thread owns a TMEM lane)
-//   8          tcgen05.mma issuer, TMEM allocator
-//   9          cuts the segments, loads K tiles by TMA
-//   10         loads Q rows (gathered, so cp.async), clears the dead output rows
-//   11         loads V tiles by TMA (with row pairs, warp 10 does; a box takes a warp some 100 cycles, and 16-token
-//              pages make 16 boxes of a tile's K and V)
-// Steps of a segment alternate between the two slots (TMEM: S0 S1 O0 O1):
-//   row group above 128 rows ("pair"): slot t holds rows 128 t .. of it and
-//     each key tile is taken by both slots in turn;
-//   up to 128 rows: both slots hold the same rows and take every other key
-//     tile, so one tile's softmax runs beside the next one's MMAs; the
-//     slots' (max, sum, O) are joined when the segment ends.
-// The rows are the M side of the MMAs.  With few rows most of M is padding,
-// but a tile's 128x128xD products take about 1000 cycles against the 2700
-// that its 64 KB need from HBM, so it costs nothing until two row tiles are
-// full; a warp without live rows skips its softmax.
+// Warp roles:
+//   0-7   softmax, two warpgroups (a thread owns a TMEM lane)
+//   8     tcgen05.mma issuer, TMEM allocator
+//   9     cuts the segments, loads K tiles by TMA
+//   10    loads Q rows (gathered, so cp.async), clears the dead output rows
+//   11    loads V tiles by TMA (a box costs a warp some 100 cycles, and 16-token
+//         pages make 16 boxes of a tile's K and V: at d = 64 out of L2 a tile took
+//         1.13 us with one warp for both, 0.70 with two).  With row pairs, where
+//         the products bound the tile, warp 10 does (1% faster than a 12th warp).
+//
+// Two forms, chosen by the rows of a kv head (its query heads times Nq):
+//   up to 128: one row tile, TMEM S0 S1 S2 O; both warpgroups take every key
+//     tile, and the fewer the rows the more copies of them the lanes hold (see
+//     the softmax); S is three tiles ahead of P V.
+//   more ("wide"): TMEM S0 S1 O0 O1, a slot for each warpgroup, taken in turn.
+//     A row group above 128 rows is a pair: slot t holds its rows 128 t .. and
+//     each key tile is taken by both slots.  A smaller one (the last of a kv
+//     head) is in both slots, which take every other key tile; their (max,
+//     sum, O) are joined when the segment ends.
+// The rows are the M side of the MMAs.  With few rows most of M is padding or
+// copies, but a tile's products take about 1000 cycles at d = 128 against the
+// 2700 that its 64 KB need from HBM, so it costs nothing until two row tiles are
+// full.
+//
+// Measured: 16 sequences of 1k to 16k keys, 36 to 64 rows on 8 kv heads, d =
+// 128, 16-token pages: 108 us, 5.66 TB/s from HBM; 8 of 8k to 32k, 256 rows: 204
+// us, 0.91 PFLOP/s, bound by the tensor and exp2 pipes (2.1 us a tile).
 //
 // P goes back to TMEM as bf16 over its S and is the A operand of P V: a
 // weight is off by at most 2^-8, as for every kernel of this library; sums,
@@ -49,8 +59,6 @@ namespace attn {
 namespace tr {
 
 constexpr int kTile = 128;        // keys per tile, rows per slot
-// Row pairs need more registers than 12 warps leave each other (168): one warp
-// less, which loads Q and V in turn.
 constexpr int threads(bool wide) { return wide ? 352 : 384; }
 constexpr int kMaxB = 2048;
 constexpr int kSegSlots = 4;      // depth of the ring of segments
