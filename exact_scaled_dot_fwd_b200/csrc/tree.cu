@@ -106,8 +106,9 @@ struct Smem {
   static constexpr int kSegInts = 8;
   static constexpr int kTmemSlot = kSeg + kSegSlots * kSegInts * 4;
   static constexpr int kAbort = kTmemSlot + 8;
-  static constexpr int kArmed = kAbort + 8;       // int [NS]: the position each stage was last filled for
-  static constexpr int kTotal = kArmed + NS * 4;   // (the base is 1024-byte aligned)
+  // int [NS + 2]: the position each stage, the tile each Q buffer was last filled for
+  static constexpr int kArmed = kAbort + 8;
+  static constexpr int kTotal = kArmed + (NS + 2) * 4;   // (the base is 1024-byte aligned)
   static_assert(kTotal <= 232448, "shared memory over the 227 KB per-CTA limit");
 };
 
@@ -246,7 +247,8 @@ __device__ __forceinline__ uint32_t ancestors32(int parent, int lane) {
 
 template <int D, bool kPaged, int kKeys>
 __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
-    tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv,
                    const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn,
                    tr::Args a) {
   using namespace tr;
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       mbar_init(&bars[i], c);
     }
     *abort_flag = 0;
-    for (int i = 0; i < NS; ++i) armed[i] = -1;
+    for (int i = 0; i < NS + 2; ++i) armed[i] = -1;
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -377,12 +379,32 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
   };
 
   // The Q rows of a segment, `part` of `parts` of them, by one warp: row r of the
-  // unit is node r % nb of head r / nb.  A lane copies one 16-byte chunk of
-  // every (32 / chunks)-th row, to each of the row's copies.
+  // unit is node r % nb of head r / nb.  Where no node is missing the rows lie
+  // together and come by TMA, a box for each copy.  Else a lane copies one
+  // 16-byte chunk of every (32 / chunks)-th row, to each of the row's copies.
   auto load_q = [&](const Seg& s, int qt, int part, int parts) -> bool {
     constexpr int kChunks = D / 8, kStep = 32 / kChunks, span = kTile / kCopies;
     const int c = lane % kChunks, rows = group_rows(s);
     const int nq = kWide && rows > kTile ? 2 : 1;
+    if (s.nb == t.Nq) {
+      for (int sl = 0; part == 0 && sl < nq; ++sl) {
+        const int buf = (qt + sl) & 1;
+        uint64_t* full = &bars[L::Q_FULL + buf];
+        if (!mbar_wait_warp(&bars[L::Q_EMPTY + buf], (((qt + sl) >> 1) & 1) ^ 1, abort_flag))
+          return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, L::kTileBytes);
+          armed[NS + buf] = qt + sl;
+          for (int cp = 0; cp < kCopies; ++cp)
+            for (int hb = 0; hb < D / 64; ++hb)
+              tma_load_3d(smem + L::kQ + buf * L::kTileBytes + hb * L::kBox + cp * span * 128, &tq,
+                          hb * 64, s.rg * 2 * kTile + sl * kTile, s.b * t.Hkv + s.h, full);
+          mbar_arrive(full);
+        }
+        __syncwarp();
+      }
+      return true;
+    }
     const int dg = kStep / s.nb, di = kStep % s.nb;
     const __nv_bfloat16* qb = t.q + ((size_t)s.b * t.Hq + (size_t)s.h * a.G) * t.Nq * D + c * 8;
     for (int sl = 0; sl < nq; ++sl) {
@@ -412,8 +434,10 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       else asm volatile("cp.async.wait_group 0;" ::: "memory");
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0)
+      if (lane == 0) {
+        if (part == 0) armed[NS + ((qt + sl) & 1)] = qt + sl;
         for (int x = parts; x < 3; ++x) mbar_arrive(&bars[L::Q_FULL + ((qt + sl) & 1)]);
+      }
     }
     return true;
   };
@@ -1293,6 +1317,8 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
   // a wait gave up)
   if (warp == 9 && lane < NS && armed[lane] >= 0)
     mbar_wait(&bars[L::FULL + lane], (armed[lane] / NS) & 1, nullptr);
+  if (warp == 10 && lane < 2 && armed[NS + lane] >= 0)
+    mbar_wait(&bars[L::Q_FULL + lane], (armed[NS + lane] >> 1) & 1, nullptr);
   if (warp == 8) {
     tc::fence_after();
     tc::dealloc(tmem, 512);
@@ -1428,7 +1454,12 @@ int launch_tree_k(const tr::Args& a, const CUtensorMap& tk, const CUtensorMap& t
   constexpr int smem = tr::Smem<D>::kTotal;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return ATTN_ECUDA;
-  const int rc = launch_programmatic(kern, dim3(a.grid), dim3(tr::threads(kKeys == 0)), smem, st, tk, tv, tkn,
+  // q as [B * Hkv, rows of a kv head, d], in boxes of one copy's rows
+  CUtensorMap tq;
+  if (make_tmap_3d_bf16(&tq, a.t.q, D, (uint64_t)a.G * a.t.Nq, (uint64_t)a.t.B * a.t.Hkv, 64,
+                        kKeys == 0 ? tr::kTile : 2 * kKeys) != ATTN_OK)
+    return ATTN_ECUDA;
+  const int rc = launch_programmatic(kern, dim3(a.grid), dim3(tr::threads(kKeys == 0)), smem, st, tq, tk, tv, tkn,
                                      tvn, a);
   if (rc != ATTN_OK) return rc;
   constexpr int HB = kJoinWarps * kJoinRows;
