@@ -493,7 +493,8 @@ def paged_plan(old_lens, new_lens, block_table, free_pages, state, page_size, N,
     i (or index[b, i], int32 [B, N], where given; negative: none), -1 where
     there is none; state_out int32 [2], the queue's new state (a tensor of its
     own: pass it as the next call's state).  Page shortage is reported by
-    device_status() (ATTN_ERANGE)."""
+    device_status() (ATTN_ERANGE); the entries that got no page are -1 and are
+    passed over when their sequence shrinks."""
     torch = _torch()
     i32 = torch.int32
     try:

@@ -13,17 +13,23 @@ namespace attn {
 // ------------------------------------------------------------------ page plan
 //
 // With h(x) = ceil(x / page_size), sequence b takes a_b = max(0, h(new) -
-// h(old)) pages and gives back r_b = max(0, h(old) - h(new)).  Its pages are
-// the queue's entries A_b .. A_b + a_b - 1 with A_b = sum_{c < b} a_c (r
-// likewise at the tail), so every entry and slot has a closed form once the
-// two prefix sums are known, and nothing has to be exchanged between CTAs:
-// each one sums the lengths below its own sequences again (8 bytes per
-// sequence, out of L2) instead of waiting for a scan kernel.
+// h(old)) pages and gives back the r_b pages among its table entries [h(new),
+// h(old)): an entry outside [0, num_pages) -- one that got no page in a
+// shortage -- is none.  Its pages are the queue's entries A_b .. A_b + a_b - 1
+// with A_b = sum_{c < b} a_c (r likewise at the tail), so every entry and slot
+// has a closed form once the two prefix sums are known, and nothing has to be
+// exchanged between CTAs: each one sums the lengths below its own sequences
+// again (8 bytes per sequence, out of L2) instead of waiting for a scan kernel.
+// Only the CTAs whose own sequences shrink, and the one that writes the state,
+// also look through the entries that the sequences below give back.
 //
-// Bound by launch latency: the whole step is a few KB to a few MB.
+// Bound by launch latency: the whole step is a few KB to a few MB (256 decode
+// steps 5.5 us, 32 prompts of 8192 tokens 6.6 us).  Where very many pages come
+// back at once, by the one CTA that looks through all of them (683 of 2048
+// requests finished, 1.0 M pages: 201 us).
 
 namespace {
-constexpr int kPlanThreads = 256;
+constexpr int kPlanAhead = 2;      // sequences of a thread whose lengths are on their way together
 constexpr int kPlanMaxS = 64;      // sequences per CTA
 constexpr int kPlanItems = 1024;   // slots per CTA, about
 }  // namespace
@@ -52,9 +58,21 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int b) {
   const int cap = a.max_pages * a.page_size;
   s.o = clamp_len(a.old_lens[b], cap);
   s.n = clamp_len(a.new_lens[b], cap);
-  s.ho = (int)(((long long)s.o + a.page_size - 1) / a.page_size);
-  s.hn = (int)(((long long)s.n + a.page_size - 1) / a.page_size);
+  // (both terms are below 2^31)
+  s.ho = (int)(((unsigned)s.o + (unsigned)a.page_size - 1u) / (unsigned)a.page_size);
+  s.hn = (int)(((unsigned)s.n + (unsigned)a.page_size - 1u) / (unsigned)a.page_size);
   return s;
+}
+
+// How many of the table entries [lo, hi) of a row are pages: the share of lane
+// `i` of `n`.
+__device__ __forceinline__ int pages_among(const int32_t* row, int lo, int hi, int i, int n,
+                                           int num_pages) {
+  int c = 0;
+#pragma unroll 8
+  for (long long j = (long long)lo + i; j < hi; j += n)
+    c += (unsigned)row[j] < (unsigned)num_pages ? 1 : 0;
+  return c;
 }
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -63,44 +81,101 @@ __device__ __forceinline__ long long warp_sum(long long x) {
   return x;
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
-  __shared__ long long s_red[4][kPlanThreads / 32];
+  constexpr int kPlanWarps = kPlanThreads / 32;
+  __shared__ long long s_red[2][kPlanWarps];
   __shared__ PlanSeq s_seq[kPlanMaxS];
   __shared__ long long s_take[kPlanMaxS], s_give[kPlanMaxS];
+  __shared__ int s_pages[kPlanMaxS];   // pages that a unit gives back
+  __shared__ long long s_all[2];       // taken and given back up to and with this CTA's sequences
+  __shared__ int s_list[3][kPlanThreads * kPlanAhead], s_listed;   // sequences that shrink
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = blockIdx.x / a.chunks, chunk = blockIdx.x - grp * a.chunks;
   const int b0 = grp * a.S;
   const int S = a.B - b0 < a.S ? a.B - b0 : a.S;
-  const bool last = blockIdx.x == 0;   // this CTA also writes the queue's new state
+  const bool last = b0 + S == a.B && chunk == 0;   // this CTA also writes the queue's new state
+  const int P = a.num_pages;
 
-  // pages taken and given back by the sequences below b0 (and by all)
-  long long tk = 0, gv = 0, tk_all = 0, gv_all = 0;
-  const int upto = last ? a.B : b0;
-  for (int b = tid; b < upto; b += kPlanThreads) {
-    const PlanSeq s = plan_seq(a, b);
-    const int t = s.hn > s.ho ? s.hn - s.ho : 0, g = s.ho > s.hn ? s.ho - s.hn : 0;
-    if (b < b0) { tk += t; gv += g; }
-    tk_all += t;
-    gv_all += g;
+  PlanSeq below[kPlanAhead];
+  auto load_below = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kPlanAhead; ++i) {
+      const int b = base + i * kPlanThreads + tid;
+      below[i] = {0, 0, 0, 0};
+      if (b < b0) below[i] = plan_seq(a, b);
+    }
+  };
+  load_below(0);
+  bool shrinks = false;
+  if (tid < S) {
+    const PlanSeq s = plan_seq(a, b0 + tid);
+    s_seq[tid] = s;
+    shrinks = s.ho > s.hn;
   }
-  tk = warp_sum(tk); gv = warp_sum(gv); tk_all = warp_sum(tk_all); gv_all = warp_sum(gv_all);
-  if (lane == 0) { s_red[0][warp] = tk; s_red[1][warp] = gv; s_red[2][warp] = tk_all; s_red[3][warp] = gv_all; }
-  if (tid < S) s_seq[tid] = plan_seq(a, b0 + tid);
+  if (tid == 0) s_listed = 0;
+  // (a group's first chunk gives back for all of them)
+  const bool gives = __syncthreads_or(shrinks) && chunk == 0;
+
+  // pages taken and given back by the sequences below b0: those that shrink
+  // are listed and looked through by 8 lanes each
+  long long tk = 0, gv = 0;
+  for (int base = 0; base < b0;) {
+#pragma unroll
+    for (int i = 0; i < kPlanAhead; ++i) {
+      const PlanSeq s = below[i];
+      if (s.hn > s.ho) tk += s.hn - s.ho;
+      if ((gives || last) && s.ho > s.hn) {
+        const int at = atomicAdd(&s_listed, 1);
+        s_list[0][at] = base + i * kPlanThreads + tid;
+        s_list[1][at] = s.hn;
+        s_list[2][at] = s.ho;
+      }
+    }
+    base += kPlanThreads * kPlanAhead;
+    if (base < b0) load_below(base);
+    if (gives || last) {
+      __syncthreads();
+      const int n = s_listed;
+      for (int i = tid >> 3; i < n; i += kPlanThreads / 8)
+        gv += pages_among(a.table + (size_t)s_list[0][i] * a.max_pages, s_list[1][i], s_list[2][i],
+                          lane & 7, 8, P);
+      __syncthreads();
+      if (tid == 0) s_listed = 0;
+      __syncthreads();
+    }
+  }
+  tk = warp_sum(tk); gv = warp_sum(gv);
+  if (lane == 0) { s_red[0][warp] = tk; s_red[1][warp] = gv; }
+
+  // What this CTA's own sequences give back, in units of a sequence (of a part
+  // of one for every warp where a CTA has a single sequence), a warp each.
+  const int parts = a.S > 1 ? 1 : kPlanWarps;
+  const int units = S * parts;
+  auto unit_lo = [&](const PlanSeq& q, int k) -> int {   // first entry of its k-th part
+    return q.hn + (int)((long long)(q.ho - q.hn) * k / parts);
+  };
+  for (int u = warp; u < units; u += kPlanWarps) {
+    const int s = a.S > 1 ? u : 0, k = u - s * parts;
+    const PlanSeq q = s_seq[s];
+    int c = 0;
+    if (gives && q.ho > q.hn)
+      c = __reduce_add_sync(0xffffffffu,
+                            pages_among(a.table + (size_t)(b0 + s) * a.max_pages, unit_lo(q, k),
+                                        unit_lo(q, k + 1), lane, 32, P));
+    if (lane == 0) s_pages[u] = c;
+  }
   __syncthreads();
   if (warp == 0) {
     long long t0 = 0, g0 = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) { t0 += s_red[0][w]; g0 += s_red[1][w]; }
-    // exclusive scan over this CTA's sequences, 32 at a time
-    for (int base = 0; base < S; base += 32) {
+    for (int w = 0; w < kPlanWarps; ++w) { t0 += s_red[0][w]; g0 += s_red[1][w]; }
+    // exclusive scans over this CTA's sequences and units, 32 at a time
+    for (int base = 0; base < units; base += 32) {
       const int i = base + lane;
-      long long t = 0, g = 0;
-      if (i < S) {
-        const PlanSeq s = s_seq[i];
-        t = s.hn > s.ho ? s.hn - s.ho : 0;
-        g = s.ho > s.hn ? s.ho - s.hn : 0;
-      }
+      long long t = 0, g = i < units ? s_pages[i] : 0;
+      if (i < S && s_seq[i].hn > s_seq[i].ho) t = s_seq[i].hn - s_seq[i].ho;
       long long xt = t, xg = g;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -108,15 +183,16 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
         const long long yg = __shfl_up_sync(0xffffffffu, xg, o);
         if (lane >= o) { xt += yt; xg += yg; }
       }
-      if (i < S) { s_take[i] = t0 + xt - t; s_give[i] = g0 + xg - g; }
+      if (i < S) s_take[i] = t0 + xt - t;
+      if (i < units) s_give[i] = g0 + xg - g;
       t0 += __shfl_sync(0xffffffffu, xt, 31);
       g0 += __shfl_sync(0xffffffffu, xg, 31);
     }
+    if (lane == 0) { s_all[0] = t0; s_all[1] = g0; }
   }
   __syncthreads();
 
   // the queue; a state from elsewhere cannot lead outside the ring
-  const int P = a.num_pages;
   int head = a.state_in[0] % P;
   if (head < 0) head += P;
   const int count = clamp_len(a.state_in[1], P);
@@ -128,8 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
   };
 
   if (last && tid == 0) {
-    long long t = 0, g = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) { t += s_red[2][w]; g += s_red[3][w]; }
+    const long long t = s_all[0], g = s_all[1];
     const long long served = t < count ? t : count;
     const long long room = P - count;
     const long long back = g < room ? g : room;
@@ -138,18 +213,36 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
     if (t > count || g > room) bad = true;
   }
 
-  // table entries taken, ring entries given back: a warp per sequence (all
-  // warps and chunks on the one sequence of a long row)
-  const int w0 = a.S > 1 ? warp : 0, wn = a.S > 1 ? kPlanThreads / 32 : 1;
+  // table entries taken: a warp per sequence (all warps and chunks on the one
+  // sequence of a long row)
+  const int w0 = a.S > 1 ? warp : 0, wn = a.S > 1 ? kPlanWarps : 1;
   const int l0 = a.S > 1 ? lane : chunk * kPlanThreads + tid;
   const int ln = a.S > 1 ? 32 : a.chunks * kPlanThreads;
   for (int s = w0; s < S; s += wn) {
     const PlanSeq q = s_seq[s];
     int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages;
     for (int j = q.ho + l0; j < q.hn; j += ln) row[j] = taken(s_take[s] + (j - q.ho));
-    for (int j = q.hn + l0; j < q.ho; j += ln) {
-      const long long m = s_give[s] + (j - q.hn);
-      if (m < P - count) a.ring[(int)(((long long)head + count + m) % P)] = row[j];
+  }
+  // pages given back, in the order of their entries, 128 at a time
+  for (int u = gives ? warp : units; u < units; u += kPlanWarps) {
+    const int s = a.S > 1 ? u : 0, k = u - s * parts;
+    const PlanSeq q = s_seq[s];
+    if (q.ho <= q.hn) continue;
+    const int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages;
+    const int hi = unit_lo(q, k + 1);
+    long long m = s_give[u];
+    for (long long j = unit_lo(q, k); j < hi; j += 128) {
+      int page[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) page[i] = j + 32 * i + lane < hi ? row[j + 32 * i + lane] : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool ok = (unsigned)page[i] < (unsigned)P;
+        const unsigned bal = __ballot_sync(0xffffffffu, ok);
+        const long long at = m + __popc(bal & ((1u << lane) - 1));
+        if (ok && at < P - count) a.ring[(int)(((long long)head + count + at) % P)] = page[i];
+        m += __popc(bal);
+      }
     }
   }
 
@@ -189,7 +282,16 @@ int launch_paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t*
   if (a.S > kPlanMaxS) a.S = kPlanMaxS;
   a.chunks = a.S > 1 ? 1 : (N + kPlanItems - 1) / kPlanItems;
   const long long grid = (long long)((B + a.S - 1) / a.S) * a.chunks;
-  return launch_programmatic(paged_plan_kernel, dim3((unsigned)grid), dim3(kPlanThreads), 0, st, a);
+  // Many sequences in few CTAs: more threads for the sums over those below a
+  // CTA's own (1000 sequences, one in ten finished: 8.9 us against 14.8 with 256;
+  // 256 that decode: 5.6 against 6.1).  Not for a few sequences (8 that decode:
+  // 4.5 us against 3.7), nor for more CTAs than SMs: with 1024 threads of 62
+  // registers an SM holds one (600 prompts of 300 tokens: 9.2 us against 6.7).
+  return B > 32 && grid <= 148
+             ? launch_programmatic(paged_plan_kernel<1024>, dim3((unsigned)grid), dim3(1024), 0,
+                                   st, a)
+             : launch_programmatic(paged_plan_kernel<256>, dim3((unsigned)grid), dim3(256), 0, st,
+                                   a);
 }
 
 // ------------------------------------------------------------------ append

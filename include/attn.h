@@ -317,8 +317,9 @@ ATTN_API size_t attn_decode_static_max_bytes(void);
  * goes from old_lens[b] to new_lens[b] tokens (both clamped to [0, max_pages
  * * page_size]); with h(x) = ceil(x / page_size) it
  *   - takes pages for block_table[b][h(old) .. h(new)) when it grows, and
- *   - gives the pages block_table[b][h(new) .. h(old)) back when it shrinks
- *     (new_lens[b] = 0: a finished request).
+ *   - gives the pages among block_table[b][h(new) .. h(old)) back when it
+ *     shrinks (new_lens[b] = 0: a finished request); an entry outside [0,
+ *     num_pages), as a shortage leaves them, is no page and is passed over.
  * Free pages form a queue in the ring free_pages[num_pages]: state_in =
  * {head, count}; pages are taken from the head in order of (b, entry) and
  * given back at the tail in the same order, so what is given back can be
@@ -337,8 +338,10 @@ ATTN_API size_t attn_decode_static_max_bytes(void);
  * tokens get slot -1, state_out holds count 0 plus the pages given back, and
  * the device status word records ATTN_ERANGE; so it does for a table entry
  * outside [0, num_pages) that a slot would need (slot -1) and for pages
- * given back beyond the ring's room (dropped).  No value makes the kernel
- * access memory outside the buffers.
+ * given back beyond the ring's room (dropped).  After a shortage a request
+ * may be finished or taken back to any length like every other: its pages
+ * return to the queue, its entries without one do not.  No value makes the
+ * kernel access memory outside the buffers.
  *   A page belongs to one sequence: the call does not count references.
  * Errors: ATTN_EINVAL (null pointers, sizes <= 0, state_in == state_out),
  * ATTN_EUNSUPPORTED (max_pages * page_size, num_pages * page_size or B * N
