@@ -1006,6 +1006,8 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
         else if (t.lse) t.lse[orow] = lse * kLn2;
       }
       tc::fence_before();
+      // the exchange went through the Q tile, which TMA may fill next
+      if constexpr (kCopies > 1) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::Q_EMPTY + (qt & 1)]);
       g += 2 * n;
