@@ -54,6 +54,7 @@
 #include "kernels.h"
 #include "tcgen05.cuh"
 #include "tile_plan.cuh"
+#include "tree_pair.cuh"
 
 namespace attn {
 namespace tr {
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
     const bool o_32B = (reinterpret_cast<uintptr_t>(t.o) & 31) == 0;
     float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
     int k = 0, g = 0, u0 = 0, qt = 0;
-    bool ok = true;
+    PairExit pair;
     Seg s;
     bool live = next_seg(k, s);
     while (!bar_vote_or(1, 256, !live)) {
@@ -796,17 +797,17 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
             }
           }
         }
-        // A wait that gives up only clears ok: the warp goes on to the vote, where
+        // A wait that gives up only marks the warp: it goes on to the next vote, where
         // it and its partner leave together.
-        if (!mbar_wait_warp(&bars[L::S_FULL + u % 3], (u / 3) & 1, abort_flag)) ok = false;
+        pair.waited(mbar_wait_warp(&bars[L::S_FULL + u % 3], (u / 3) & 1, abort_flag));
         // P V of tile u - 2 (each of its barrier's phases is waited for, in order)
-        if (u >= 2 && !mbar_wait_warp(&bars[L::O_FULL + (u & 1)], ((u - 2) >> 1) & 1, abort_flag))
-          ok = false;
+        if (u >= 2)
+          pair.waited(mbar_wait_warp(&bars[L::O_FULL + (u & 1)], ((u - 2) >> 1) & 1, abort_flag));
         tc::fence_after();
         if (masked && valid < kTile && hf == 0) {
           // values that do not exist: anything may be stored there
           const int pos = v_pos(g, j, n, false);
-          if (!mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag)) ok = false;
+          pair.waited(mbar_wait_warp(&bars[L::FULL + pos % NS], (pos / NS) & 1, abort_flag));
           if (r >= valid) {
             const bool grouped = kPaged && D == 128 && jt < np;
             uint8_t* vt = smem + L::kKV + (pos % NS) * L::kTileBytes +
@@ -866,18 +867,15 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
         // The two threads of a lane agree.  (The vote is also what lets the
         // second one write its P over scores that the first has read.)
         const bool need = !dead && m_tile > m_run + kRescaleLog2;
-        if (bar_vote_or(3 + qr, 64, need || j == 0 || !ok)) {
-          ml[hf * kTile + r] = make_float2(m_tile, ok ? 1.f : 0.f);
+        if (bar_vote_or(3 + qr, 64, need || j == 0 || !pair.ok())) {
+          ml[hf * kTile + r] = make_float2(m_tile, pair.ok() ? 1.f : 0.f);
           asm volatile("bar.sync %0, 64;" ::"r"(3 + qr) : "memory");
           const float2 other = ml[(hf ^ 1) * kTile + r];
-          if (!__all_sync(0xffffffffu, ok && other.y != 0.f)) {
-            ok = false;
-            return;
-          }
+          if (!pair.meet(__all_sync(0xffffffffu, other.y != 0.f))) return;
           const float m_row = fmaxf(m_tile, other.x);
           const float m_new = !dead && m_row > m_run + kRescaleLog2 ? m_row : m_run;
           if (j > 0) {
-            if (!mbar_wait_warp(&bars[L::O_FULL + ((u - 1) & 1)], ((u - 1) >> 1) & 1, abort_flag)) ok = false;
+            pair.waited(mbar_wait_warp(&bars[L::O_FULL + ((u - 1) & 1)], ((u - 1) >> 1) & 1, abort_flag));
             tc::fence_after();
             const float f = (m_new > m_run && m_run != -INFINITY) ? exp2_approx(m_run - m_new) : 1.f;
             l_run *= f;
@@ -915,7 +913,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
         tc::fence_before();
         mbar_arrive(&bars[L::P_FULL + u % 3]);
       };
-      for (int j = 0; ok && j < n; ++j) {
+      for (int j = 0; pair.more(j, n); ++j) {
         const int jt = s.j0 + j;                           // tile of the unit
         const int valid = jt < np ? s.L - jt * kTile : s.nb - (jt - np) * kTile;
         if (jt >= np || valid < kTile) tile(std::true_type(), j, jt, valid);
@@ -924,12 +922,12 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       // ---- segment end
       asm volatile("bar.sync %0, 64;" ::"r"(3 + qr) : "memory");   // (maxima of the last vote read)
       ml[hf * kTile + r] = make_float2(m_run, l_run);
-      if (ok) {
+      if (pair.ok()) {
         const int u = u0 + n - 1;
-        if (!mbar_wait_warp(&bars[L::O_FULL + (u & 1)], (u >> 1) & 1, abort_flag)) ok = false;
+        pair.waited(mbar_wait_warp(&bars[L::O_FULL + (u & 1)], (u >> 1) & 1, abort_flag));
       }
       // (also orders the exchange; every softmax thread leaves on the same vote)
-      if (bar_vote_or(2, 256, !ok)) break;
+      if (bar_vote_or(2, 256, !pair.ok())) break;
       tc::fence_after();
       float m = -INFINITY, l = 0.f;
       for (int c = 0; c < copies; ++c) m = fmaxf(m, ml[c * per_copy * 32 + lr].x);
