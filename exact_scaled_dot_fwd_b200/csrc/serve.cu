@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
   const int P = a.num_pages;
 
   PlanSeq below[kPlanAhead];
-  auto load_below = [&](int base) {
+  auto load_below = [&](unsigned base) {   // (unsigned: B may be just below 2^31)
 #pragma unroll
     for (int i = 0; i < kPlanAhead; ++i) {
-      const int b = base + i * kPlanThreads + tid;
+      const unsigned b = base + i * kPlanThreads + tid;
       below[i] = {0, 0, 0, 0};
-      if (b < b0) below[i] = plan_seq(a, b);
+      if (b < (unsigned)b0) below[i] = plan_seq(a, (int)b);
     }
   };
   load_below(0);
@@ -122,20 +122,20 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
   // pages taken and given back by the sequences below b0: those that shrink
   // are listed and looked through by 8 lanes each
   long long tk = 0, gv = 0;
-  for (int base = 0; base < b0;) {
+  for (unsigned base = 0; base < (unsigned)b0;) {
 #pragma unroll
     for (int i = 0; i < kPlanAhead; ++i) {
       const PlanSeq s = below[i];
       if (s.hn > s.ho) tk += s.hn - s.ho;
       if ((gives || last) && s.ho > s.hn) {
         const int at = atomicAdd(&s_listed, 1);
-        s_list[0][at] = base + i * kPlanThreads + tid;
+        s_list[0][at] = (int)(base + i * kPlanThreads + tid);
         s_list[1][at] = s.hn;
         s_list[2][at] = s.ho;
       }
     }
     base += kPlanThreads * kPlanAhead;
-    if (base < b0) load_below(base);
+    if (base < (unsigned)b0) load_below(base);
     if (gives || last) {
       __syncthreads();
       const int n = s_listed;
@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
   for (int s = w0; s < S; s += wn) {
     const PlanSeq q = s_seq[s];
     int32_t* row = a.table + (size_t)(b0 + s) * a.max_pages;
-    for (int j = q.ho + l0; j < q.hn; j += ln) row[j] = taken(s_take[s] + (j - q.ho));
+    // (unsigned: a row may end just below 2^31)
+    for (unsigned j = (unsigned)q.ho + l0; j < (unsigned)q.hn; j += ln)
+      row[j] = taken(s_take[s] + (j - (unsigned)q.ho));
   }
   // pages given back, in the order of their entries, 128 at a time
   for (int u = gives ? warp : units; u < units; u += kPlanWarps) {
