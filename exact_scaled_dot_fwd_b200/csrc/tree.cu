@@ -55,11 +55,11 @@
 #include "tcgen05.cuh"
 #include "tile_plan.cuh"
 #include "tree_pair.cuh"
+#include "tree_tiles.cuh"
 
 namespace attn {
 namespace tr {
 
-constexpr int kTile = 128;        // keys per tile, rows per slot
 constexpr int threads(bool wide) { return wide ? 352 : 384; }
 constexpr int kMaxB = 2048;
 constexpr int kSegSlots = 4;      // depth of the ring of segments
@@ -140,7 +140,7 @@ struct Seg {
   int j0, n;          // key tiles [j0, j0 + n); n = 0 ends the stream
   int L, nb;          // cached keys, live nodes
   int flags;          // 1: the CTA's first segment, 2: the whole unit
-  __device__ __forceinline__ int np() const { return (L + kTile - 1) / kTile; }
+  __device__ __forceinline__ int np() const { return key_tiles(L); }
 };
 
 __device__ __forceinline__ int cached_len(const TreeArgs& t, int b) {
@@ -159,7 +159,7 @@ struct Split {
   long long head;      // cost of a kv head
   __device__ __forceinline__ Split(int L, int nb, int G, int cost_unit) : cu(cost_unit) {
     const int rows = G * nb;
-    nt = nb > 0 ? (L + kTile - 1) / kTile + (nb + kTile - 1) / kTile : 0;
+    nt = nb > 0 ? key_tiles(L) + key_tiles(nb) : 0;
     nrg = (rows + 2 * kTile - 1) / (2 * kTile);
     w_last = rows - (nrg - 1) * 2 * kTile > kTile ? kCostPair : kCostTile;
     head = nb > 0 ? (long long)(nrg - 1) * unit(kCostPair) + unit(w_last) : 0;
@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
     // this lane's entry of the block table for tile j (-1: a page past the
     // cached keys), looked up two tiles before it is needed
     auto entry = [&](int j) -> int {
-      const int pg = (s.j0 + j) * npg + lane;
-      return j < n && lane < npg && pg * t.page_size < s.L ? table[pg] : -1;
+      const int pg = j < n ? tile_page(s.j0 + j, lane, np, npg, t.page_size, s.L) : -1;
+      return pg >= 0 ? table[pg] : -1;
     };
     int e0 = kPaged ? entry(0) : 0, e1 = kPaged ? entry(1) : 0;
     for (int j = 0; j < n; ++j) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
       } else if constexpr (kPaged) {
         if (lane < npg) {
           // (pages past the cached keys: the row past the cache, zeros)
-          const int row = (jt * npg + lane) * t.page_size < s.L
+          const int row = tile_page(jt, lane, np, npg, t.page_size, s.L) >= 0
                               ? paged_cache_row(e0, t.num_pages, t.Hkv, s.h, t.page_size, a.oob_row)
                               : a.oob_row;
           if constexpr (D == 128) tma_load_4d(dst + lane * t.page_size * 256, map, row >> 3, full);
