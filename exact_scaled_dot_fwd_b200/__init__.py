@@ -440,20 +440,22 @@ def _refuse(ref, args):
 
 class _On:
     """The device and stream of a call.  Makes the device current while the
-    call runs; what is allocated for another stream than the current one is
-    marked as used there, so that the caching allocator keeps its memory until
-    that stream has passed the call."""
+    call runs.  What is allocated for another stream than the current one comes
+    from that stream's memory (a block of the current stream's may still be in
+    use by work queued there); what is returned is marked as used by the current
+    stream too, so that, once freed, it is kept until that stream has passed."""
 
-    __slots__ = ("guard", "other", "raw")
+    __slots__ = ("guard", "other", "raw", "current")
 
     def __init__(self, dev, stream):
         torch = _torch()
-        self.guard = self.other = None
+        self.guard = self.other = self.current = None
         if torch.cuda.current_device() != dev:
             self.guard = torch.cuda.device(dev)
         self.raw = torch._C._cuda_getCurrentRawStream(dev)
         if stream is not None and stream.cuda_stream != self.raw:
             self.other, self.raw = stream, stream.cuda_stream
+            self.current = torch.cuda.current_stream(dev)
 
     def __enter__(self):
         if self.guard is not None:
@@ -465,17 +467,17 @@ class _On:
             self.guard.__exit__(*exc)
         return False
 
-    def new(self, like, shape, dtype):
-        t = like.new_empty(shape, dtype=dtype)
-        if self.other is not None:
-            t.record_stream(self.other)
+    def new(self, like, shape, dtype, returned=True):
+        if self.other is None:
+            return like.new_empty(shape, dtype=dtype)
+        with _torch().cuda.stream(self.other):
+            t = like.new_empty(shape, dtype=dtype)
+        if returned:
+            t.record_stream(self.current)
         return t
 
     def like(self, t):      # of a contiguous tensor
-        t = _torch().empty_like(t)
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
+        return _torch().empty_like(t) if self.other is None else self.new(t, t.shape, t.dtype)
 
 
 def _data(t):
@@ -730,7 +732,7 @@ def attn_fwd_tree(q, k_cache, v_cache, key_lens, k_new, v_new, parents, new_lens
             ws_bytes = _tree_ws_bytes.get(key)
             if ws_bytes is None:
                 ws_bytes = _tree_ws_bytes[key] = L.attn_tree_workspace_size(B, Hq, Hkv, Nq, d)
-            workspace = on.new(q, (max(ws_bytes, 256),), torch.uint8)
+            workspace = on.new(q, (max(ws_bytes, 256),), torch.uint8, returned=False)
         else:
             ws_bytes = workspace.numel()
         rc = L.attn_fwd_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
