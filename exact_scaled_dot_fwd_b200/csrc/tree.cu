@@ -19,7 +19,8 @@
 //   0-7   softmax, two warpgroups (a thread owns a TMEM lane)
 //   8     tcgen05.mma issuer, TMEM allocator
 //   9     cuts the segments, loads K tiles by TMA
-//   10    loads Q rows (gathered, so cp.async), clears the dead output rows
+//   10    loads Q rows (by TMA; where nodes are missing, gathered by cp.async),
+//         clears the dead output rows
 //   11    loads V tiles by TMA (a box costs a warp some 100 cycles, and 16-token
 //         pages make 16 boxes of a tile's K and V: at d = 64 out of L2 a tile took
 //         1.13 us with one warp for both, 0.70 with two).  With row pairs, where
@@ -40,8 +41,12 @@
 // full.
 //
 // Measured: 16 sequences of 1k to 16k keys, 36 to 64 rows on 8 kv heads, d =
-// 128, 16-token pages: 108 us, 5.66 TB/s from HBM; 8 of 8k to 32k, 256 rows: 204
-// us, 0.91 PFLOP/s, bound by the tensor and exp2 pipes (2.1 us a tile).
+// 128, 16-token pages: 109 us cool, 125 after 0.6 s of load; the main kernel reads
+// 5.66 TB/s from HBM.  8 of 8k to 32k, 256 rows: 203 us cool (0.91 PFLOP/s), 244
+// after load.  Row pairs take 1.9 to 2.2 us a tile and 25 to 30 us beside their
+// tiles; a tile's products are 1.5 us and its exponentials 1.0, so neither pipe is
+// full: what bounds them is the chain of a slot (two passes over S, the hand-off,
+// P V, the next S), as in the prefill kernel.
 //
 // P goes back to TMEM as bf16 over its S and is the A operand of P V: a
 // weight is off by at most 2^-8, as for every kernel of this library; sums,
@@ -1123,11 +1128,12 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
           mbar_arrive(&bars[L::P_FULL + sl]);
           continue;
         }
-        // An unmasked tile after the slot's first: the running max usually
-        // stands (O is rescaled only when a score passes it by more than 8
-        // in log2 units), so P is computed with it from a single read of S
-        // and kept if no live row of the warp needs a rescale.  (The branch
-        // is on what the whole warp shares: tcgen05 moves are warp-wide.)
+        // An unmasked tile: two passes over S in halves, one for the tile's
+        // maximum, one for P with the running maximum, which usually stands (O
+        // is rescaled only when a live row of the warp passes it by more than 8
+        // in log2 units).  Nothing of S is held across the passes: there are no
+        // registers for it.  (The branch is on what the whole warp shares:
+        // tcgen05 moves are warp-wide.)
         if (!masked) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1169,13 +1175,12 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
           mbar_arrive(&bars[L::P_FULL + sl]);
           continue;
         }
-        // two passes over S, in chunks of 32 keys: a chunk that no row of the
-        // warp sees is skipped, one that every row sees takes no mask
+        // A masked tile: two passes over S in chunks of 32 keys; a chunk that no
+        // row of the warp sees is skipped.
         float mx = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const uint32_t w = !masked ? 0xffffffffu
-                                     : (c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3]);
+          const uint32_t w = c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3];
           if (!__any_sync(0xffffffffu, w != 0u)) continue;
           float sv[32];
           tc::ld32f(scol + 32 * c, sv);
@@ -1190,8 +1195,7 @@ __global__ void __launch_bounds__(tr::threads(kKeys == 0), 1)
         float rs = 0.f;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          const uint32_t w = !masked ? 0xffffffffu
-                                     : (c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3]);
+          const uint32_t w = c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3];
           uint32_t pk[16];
           if (!__any_sync(0xffffffffu, w != 0u)) {
 #pragma unroll
