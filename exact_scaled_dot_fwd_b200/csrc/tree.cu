@@ -42,7 +42,7 @@
 //
 // Measured: 16 sequences of 1k to 16k keys, 36 to 64 rows on 8 kv heads, d =
 // 128, 16-token pages: 109 us cool, 125 after 0.6 s of load; the main kernel reads
-// 5.66 TB/s from HBM.  8 of 8k to 32k, 256 rows: 203 us cool (0.91 PFLOP/s), 244
+// 5.7 TB/s from HBM.  8 of 8k to 32k, 256 rows: 203 us cool (0.91 PFLOP/s), 244
 // after load.  Row pairs take 1.9 to 2.2 us a tile and 25 to 30 us beside their
 // tiles; a tile's products are 1.5 us and its exponentials 1.0, so neither pipe is
 // full: what bounds them is the chain of a slot (two passes over S, the hand-off,
