@@ -86,3 +86,26 @@ def test_results_that_the_current_stream_still_reads(torch, name):
     torch.cuda.synchronize()
     for a, b in zip(copies, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["append", "tree"])
+def test_captured_on_a_forked_stream(torch, name):
+    """A capture that forks to a side stream for the call and joins it again."""
+    call = calls(torch, name)()
+    side = torch.cuda.Stream()
+    want = call(None)
+    call(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(3):
+        for t in (*got, *copies):
+            t.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, copies, want):
+            assert torch.equal(a, c) and torch.equal(b, c)
