@@ -26,7 +26,7 @@ namespace attn {
 // Bound by launch latency: the whole step is a few KB to a few MB (256 decode
 // steps 5.5 us, 32 prompts of 8192 tokens 6.6 us).  Where very many pages come
 // back at once, by the one CTA that looks through all of them (683 of 2048
-// requests finished, 1.0 M pages: 201 us).
+// requests finished, 1.0 M pages: 121 us).
 
 namespace {
 constexpr int kPlanAhead = 2;      // sequences of a thread whose lengths are on their way together
@@ -65,13 +65,24 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int b) {
 }
 
 // How many of the table entries [lo, hi) of a row are pages: the share of lane
-// `i` of `n`.
+// `i` of `n` (at least 4), in 16-byte loads between the row's odd ends.
 __device__ __forceinline__ int pages_among(const int32_t* row, int lo, int hi, int i, int n,
                                            int num_pages) {
+  const int32_t* p = row + lo;
+  const int len = hi > lo ? hi - lo : 0;
+  int head = (int)((0u - (unsigned)(reinterpret_cast<uintptr_t>(p) >> 2)) & 3u);
+  if (head > len) head = len;
+  const int whole = (len - head) >> 2, tail = head + 4 * whole;
+  auto is_page = [&](int e) { return (unsigned)e < (unsigned)num_pages ? 1 : 0; };
   int c = 0;
-#pragma unroll 8
-  for (long long j = (long long)lo + i; j < hi; j += n)
-    c += (unsigned)row[j] < (unsigned)num_pages ? 1 : 0;
+  if (i < head) c += is_page(p[i]);
+  if (i < len - tail) c += is_page(p[tail + i]);
+  const int4* q = reinterpret_cast<const int4*>(p + head);
+#pragma unroll 4
+  for (int j = i; j < whole; j += n) {
+    const int4 e = q[j];
+    c += is_page(e.x) + is_page(e.y) + is_page(e.z) + is_page(e.w);
+  }
   return c;
 }
 
@@ -285,10 +296,10 @@ int launch_paged_plan(const int32_t* old_lens, const int32_t* new_lens, int32_t*
   a.chunks = a.S > 1 ? 1 : (N + kPlanItems - 1) / kPlanItems;
   const long long grid = (long long)((B + a.S - 1) / a.S) * a.chunks;
   // Many sequences in few CTAs: more threads for the sums over those below a
-  // CTA's own (1000 sequences, one in ten finished: 8.9 us against 14.8 with 256;
-  // 256 that decode: 5.6 against 6.1).  Not for a few sequences (8 that decode:
-  // 4.5 us against 3.7), nor for more CTAs than SMs: with 1024 threads of 62
-  // registers an SM holds one (600 prompts of 300 tokens: 9.2 us against 6.7).
+  // CTA's own (1000 sequences, one in ten finished: 8.0 us against 12.7 with 256;
+  // 256 that decode: 5.6 against 5.9).  Not for a few sequences (8 that decode:
+  // 4.5 us against 3.7), nor for more CTAs than SMs: with 1024 threads of 64
+  // registers an SM holds one (600 prompts of 300 tokens: 9.4 us against 6.5).
   return B > 32 && grid <= 148
              ? launch_programmatic(paged_plan_kernel<1024>, dim3((unsigned)grid), dim3(1024), 0,
                                    st, a)
